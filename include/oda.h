@@ -279,6 +279,110 @@ int oda_recall_loss_grad(const float* h_prev, const float* emb, const void* h_lo
                          float* loss_out, float* dw1, float* db1, float* dw2, float* db2,
                          void* ws, size_t ws_bytes, void* stream);
 
+/* ---- 4-bit KV cache (no counterpart in the papers: [ODA] 개발자 관점 keeps the whole history
+ *      on the GPU, here in 144 bytes per position and KV head instead of 512) ----------------
+ * One (page, KV head) is one run of ODA_KV4_PAGE_BYTES bytes: K codes [16 tokens][64 B], V codes
+ * [16][64 B], meta [16][4 words]. A row's 128 dims are two groups of 64 (dims 0-63, 64-127). The
+ * little-endian 32-bit word 2 i + g of a row holds dims 64 g + 8 i .. + 7 in its nibbles, lowest
+ * first. A token's meta words are (K group 0, K group 1, V group 0, V group 1), each a bf16 scale in
+ * the low half and a bf16 minimum in the high half; code c stands for minimum + c * scale.
+ * Quantising a group: minimum = its least value, scale = the bf16 next at or above (max - min) / 15,
+ * c = rint((x - minimum) / scale), halves to even; a value reads back within scale / 2. A group
+ * that holds an infinity or a NaN, or spans more than the largest fp32, reads back as NaN. */
+enum { ODA_KV4_PAGE_BYTES = 2304, ODA_KV4_GROUP = 64 };
+typedef struct {
+  void* cache;                  /* uint8 [num_blocks][num_kv_heads][ODA_KV4_PAGE_BYTES]        */
+  const int32_t* block_table;   /* these as in oda_kv                                         */
+  const int32_t* seq_lens;
+  int32_t batch;
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* must be 128                                               */
+  int32_t block_size;           /* must be 16                                                */
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks;
+  int32_t* dev_status;
+  unsigned long long* stats;
+} oda_kv4;
+
+/* Quantise rows into the cache. k_new, v_new: bf16 rows of [num_kv_heads][128], row i at
+ * k_new + i * k_stride elements (strides multiples of 8, at least num_kv_heads * 128: the K part of a
+ * fused projection's output can be passed as it is); 16-byte aligned. cu_rows null: num_rows = batch
+ * and row b goes to slot t = seq_lens[b] - 1 of sequence b. Otherwise cu_rows is device int32
+ * [batch + 1], ascending: rows cu_rows[b] .. cu_rows[b + 1] - 1 go to the last slots of sequence b, the
+ * last of them to slot t (seq_lens counts them already), none for an empty range; rows outside every
+ * range are ignored. gate (nullable int32 [batch]): sequences with gate[b] == 0 are left alone. A
+ * sequence with a bad length or more rows than tokens is skipped (ODA_DEV_BAD_LEN), a row whose page is
+ * bad too (ODA_DEV_BAD_BLOCK). */
+int oda_kv4_append(const oda_kv4* kv, const void* k_new, const void* v_new, int64_t k_stride,
+                   int64_t v_stride, int32_t num_rows, const int32_t* cu_rows, const int32_t* gate,
+                   void* stream);
+
+/* Read rows back: the values the cache holds in the slots that oda_kv4_append with the same
+ * num_rows and cu_rows would write, as minimum + c * scale rounded to out_dtype (ODA_F32, ODA_BF16).
+ * k_out, v_out: dense [num_rows][num_kv_heads][128], 16-byte aligned; rows of no slot keep their
+ * contents. */
+int oda_kv4_read(const oda_kv4* kv, void* k_out, void* v_out, int32_t out_dtype, int32_t num_rows,
+                 const int32_t* cu_rows, void* stream);
+
+/* Decode attention over the 4-bit cache under any rule (arguments and results as oda_decode; k_new,
+ * v_new dense bf16 [batch][num_kv_heads][128] are quantised into slot t and attended as they read
+ * back). Weights, sums and the output are fp32 until the last rounding. ws: at least
+ * oda_kv4_decode_workspace_size() bytes, zeroed once, as for the other decode calls. */
+int oda_kv4_decode_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
+                                  size_t* bytes);
+int oda_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q, int32_t num_q_heads,
+                   float scale, const void* k_new, const void* v_new, void* out, int32_t out_dtype,
+                   float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- decode with accumulated attention weight, and eviction by it (no counterpart in the papers;
+ *      the Full rule's cost without it is the whole history) --------------------------------
+ * oda_decode / oda_kv4_decode, and
+ *   mass_out[b][g][p] = mass_in[b][g][p] + sum over the query heads of KV head g of the softmax weight of
+ *                       position p (0 where p is not visible)
+ * for 0 <= p < seq_lens[b]; other positions, and the rows of a sequence that is gated off or in error,
+ * keep their contents. mass_in, mass_out: fp32 [batch][num_kv_heads][mass_tokens], 16-byte aligned,
+ * mass_tokens a multiple of 4 and at least 16 * max_blocks_per_seq. mass_in may be mass_out (only
+ * visible positions are then touched) or NULL (zero); it may not overlap it otherwise. ws: at least the
+ * matching workspace size (it holds a score per query head and position), zeroed once. With a keep list
+ * that is not strictly ascending the sequence's mass is unspecified. Two kernel launches. */
+int oda_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
+                                   int32_t max_blocks_per_seq, size_t* bytes);
+int oda_kv4_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
+                                       int32_t max_blocks_per_seq, size_t* bytes);
+int oda_decode_mass(const oda_kv* kv, const oda_visibility* vis, const void* q, int32_t num_q_heads,
+                    float scale, const void* k_new, const void* v_new, void* out, int32_t out_dtype,
+                    float* lse, const float* mass_in, float* mass_out, int64_t mass_tokens, void* ws,
+                    size_t ws_bytes, void* stream);
+int oda_kv4_decode_mass(const oda_kv4* kv, const oda_visibility* vis, const void* q,
+                        int32_t num_q_heads, float scale, const void* k_new, const void* v_new,
+                        void* out, int32_t out_dtype, float* lse, const float* mass_in,
+                        float* mass_out, int64_t mass_tokens, void* ws, size_t ws_bytes, void* stream);
+
+/* Evict: every sequence of more than `budget` tokens is cut down to `budget`. Each KV head keeps its
+ * first `sink` slots, its last `recent` slots, and of the others the budget - sink - recent of the largest
+ * mass (ties to the lower slot; -0 counts as 0), in ascending slot order, as slots 0 .. budget - 1 of the
+ * destination pages dst_block_table (int32 [batch][dst_blocks_per_seq], page ids of the same cache,
+ * holding min(budget, 16 * max_blocks_per_seq) tokens at least). Shorter sequences keep every slot.
+ *   kept         : int32 [batch][num_kv_heads][budget], the old slot of every kept one, then -1
+ *   mass_out     : fp32 [batch][num_kv_heads][mass_tokens]: the kept slots' mass, then 0 up to the old length
+ *   seq_lens_out : int32 [batch], the new lengths
+ * In place: dst_block_table may be kv->block_table (dst_blocks_per_seq is then max_blocks_per_seq),
+ * mass_out may be mass, seq_lens_out may be kv->seq_lens. Otherwise destination pages are no pages of
+ * any sequence's history. No page may belong to two sequences of the batch that are written. A sequence
+ * with gate[b] == 0 (gate nullable), a bad length (ODA_DEV_BAD_LEN) or a bad page id in either table
+ * (ODA_DEV_BAD_BLOCK) is left as it is, with its old length in seq_lens_out. sink, recent >= 0,
+ * sink + recent <= budget, budget >= 1, mass_tokens >= 16 * max_blocks_per_seq. ws:
+ * oda_kv_evict_workspace_size() bytes, zeroed once; left zeroed. */
+int oda_kv_evict_workspace_size(int32_t batch, size_t* bytes);
+int oda_kv_evict(const oda_kv* kv, const float* mass, int64_t mass_tokens, int32_t sink, int32_t recent,
+                 int32_t budget, const int32_t* gate, const int32_t* dst_block_table,
+                 int32_t dst_blocks_per_seq, int32_t* kept, float* mass_out, int32_t* seq_lens_out,
+                 void* ws, size_t ws_bytes, void* stream);
+int oda_kv4_evict(const oda_kv4* kv, const float* mass, int64_t mass_tokens, int32_t sink,
+                  int32_t recent, int32_t budget, const int32_t* gate, const int32_t* dst_block_table,
+                  int32_t dst_blocks_per_seq, int32_t* kept, float* mass_out, int32_t* seq_lens_out,
+                  void* ws, size_t ws_bytes, void* stream);
+
 /* ---- Step runtime: one whole ODA decode step as one CUDA graph ([ODA] 개발자 관점: Local,
  *      the FP32 recall head and the conditional Full recompute in one GPU execution stream,
  *      e.g. CUDA Graphs) ----------------------------------------------------------------

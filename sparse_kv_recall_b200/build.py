@@ -22,8 +22,10 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "liboda.so")
 
 SOURCES = ["oda_decode.cu", "oda_chain.cu", "oda_append.cu", "oda_recall.cu", "oda_graph.cu", "oda_noalloc.cu",
-           "oda_merge.cu", "oda_schedule.cu", "oda_train.cu", "oda_api.cpp"]
-HEADERS = ["oda_common.cuh", "oda_plan.cuh", "oda_internal.h", "oda_recall.cuh", "oda_decode.cuh"]
+           "oda_merge.cu", "oda_schedule.cu", "oda_train.cu", "oda_kv4_cache.cu", "oda_kv4_decode.cu",
+           "oda_mass.cu", "oda_evict.cu", "oda_api.cpp"]
+HEADERS = ["oda_common.cuh", "oda_plan.cuh", "oda_internal.h", "oda_recall.cuh", "oda_decode.cuh",
+           "oda_kv4.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -7,7 +7,7 @@
 
 namespace oda {
 
-template <int G>
+template <int G, bool kScores = false>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_align, s_last;
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(const Deco
   if (p.wait_first) dep_wait();
   const long long T = split_prologue(p.plan, p.batch, p.hkv, sm, p.status);
   RingState rs{0u, false, false};
-  decode_pass<G>(p, sm, T, rs, dep_wait);
+  decode_pass<G, kScores>(p, sm, T, rs, dep_wait);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -417,7 +417,7 @@ int check_visibility(const oda_kv* kv, const oda_visibility* v) {
   }
 }
 
-static PlanArgs plan_args(const oda_kv* kv, const oda_visibility& v) {
+PlanArgs plan_args(const oda_kv* kv, const oda_visibility& v) {
   PlanArgs a;
   a.seq_lens = kv->seq_lens;
   a.block_table = kv->block_table;
@@ -447,13 +447,10 @@ oda_visibility visibility(int mode) {
   return v;
 }
 
-int decode_params(const oda_kv* kv, const oda_visibility& vis, const void* q, int hq,
-                  float scale, const void* k_new, const void* v_new, void* out, int out_dtype,
-                  float* lse, void* ws, size_t ws_bytes, DecodeParams* pp) {
-  int rc = check_kv(kv);
-  if (rc != ODA_OK) return rc;
-  if ((rc = check_visibility(kv, &vis)) != ODA_OK) return rc;
-  int G = 0;
+int check_decode_args(const oda_kv* kv, const oda_visibility& vis, const void* q, int hq, float scale,
+                      const void* k_new, const void* v_new, const void* out, int out_dtype,
+                      const float* lse, const void* ws) {
+  int rc, G = 0;
   if ((rc = group_of(kv, hq, &G)) != ODA_OK) return rc;
   if (out_dtype != ODA_F32 && out_dtype != ODA_BF16) return ODA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !isfinite(scale)) return ODA_ERR_INVALID_ARG;
@@ -467,6 +464,18 @@ int decode_params(const oda_kv* kv, const oda_visibility& vis, const void* q, in
   if (!aligned16(ws) || !aligned_or_null(out, out_dtype == ODA_BF16 ? 2 : 4) ||
       !aligned_or_null(lse, 4))
     return ODA_ERR_INVALID_ARG;
+  return ODA_OK;
+}
+
+int decode_params(const oda_kv* kv, const oda_visibility& vis, const void* q, int hq,
+                  float scale, const void* k_new, const void* v_new, void* out, int out_dtype,
+                  float* lse, void* ws, size_t ws_bytes, DecodeParams* pp) {
+  int rc = check_kv(kv);
+  if (rc != ODA_OK) return rc;
+  if ((rc = check_visibility(kv, &vis)) != ODA_OK) return rc;
+  rc = check_decode_args(kv, vis, q, hq, scale, k_new, v_new, out, out_dtype, lse, ws);
+  if (rc != ODA_OK || kv->batch == 0) return rc;
+  const int G = hq / kv->num_kv_heads;
   DeviceInfo di;
   if ((rc = current_device_info(&di)) != ODA_OK) return rc;
   const int grid = grid_size(di);
@@ -496,6 +505,8 @@ int decode_params(const oda_kv* kv, const oda_visibility& vis, const void* q, in
   p.status = kv->dev_status;
   p.stats = kv->stats;
   p.wait_first = 0;
+  p.scores = nullptr;
+  p.score_cap = 0;
   p.wait_ns = test_wait_ns();
   p.test_stall = test_stall() == ODA_STALL_DECODE_RING ? 1
                  : test_stall() == ODA_STALL_LOCAL_PUSH ? 2
@@ -542,6 +553,39 @@ int launch_decode(const oda_kv* kv, const oda_visibility& vis, const void* q, in
       break;
   }
   return cuda_status(e);
+}
+
+template <int G>
+static int launch_scores_kernel(const DecodeParams& p, const DeviceInfo& di, cudaStream_t st) {
+  static bool done[64] = {false};
+  if (di.device < 0 || di.device >= 64) return ODA_ERR_CUDA;
+  if (!done[di.device]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(decode_kernel<G, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)decode_smem_bytes(G));
+    if (e != cudaSuccess) return cuda_status(e);
+    done[di.device] = true;
+  }
+  decode_kernel<G, true><<<grid_size(di), kThreads, decode_smem_bytes(G), st>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+int launch_decode_scores(const oda_kv* kv, const oda_visibility& vis, const void* q, int hq,
+                         float scale, const void* k_new, const void* v_new, void* out, int out_dtype,
+                         float* lse, float* scores, int cap, void* ws, size_t ws_bytes, void* stream) {
+  DecodeParams p;
+  int rc = decode_params(kv, vis, q, hq, scale, k_new, v_new, out, out_dtype, lse, ws, ws_bytes, &p);
+  if (rc != ODA_OK || kv->batch == 0) return rc;
+  p.scores = scores;
+  p.score_cap = cap;
+  DeviceInfo di;
+  if ((rc = current_device_info(&di)) != ODA_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (hq / kv->num_kv_heads) {
+    case 1: return launch_scores_kernel<1>(p, di, st);
+    case 2: return launch_scores_kernel<2>(p, di, st);
+    default: return launch_scores_kernel<4>(p, di, st);
+  }
 }
 
 }  // namespace oda

@@ -51,6 +51,8 @@ struct DecodeParams {
                                // that no copy delivers, so that its bounded wait runs out;
                                // 2 = the Local cluster kernel's first cluster's rank 1
                                // withholds its partial, so that rank 0's inbox wait runs out
+  float* scores;               // decode_pass<G, true>: [batch][hq][score_cap], base 2
+  int score_cap;
 };
 
 // ---- reduce-scatter of C values over the 16 lanes of a half-warp ------------------------
@@ -109,12 +111,13 @@ __device__ __forceinline__ f2_t bf16x2_widen(uint32_t w) {
 
 // One page: scores, online-softmax update, P.V accumulation. q2[gg][j] holds the scaled
 // query dims (8 li + 2j, 8 li + 2j + 1) of head gg; acc[gg][j] the same dims of its P.V sum.
-template <int G>
+template <int G, bool kScores = false>
 __device__ __forceinline__ void page_step(const unsigned char* stage, const f2_t (&q2)[G][4],
                                           float (&m_run)[Vpl<G>::value],
                                           float (&l_run)[Vpl<G>::value], f2_t (&acc)[G][4],
                                           float* ps, const SeqPlan& sp, int lp, int lane,
-                                          unsigned& rows_vis) {
+                                          unsigned& rows_vis, float* scores = nullptr,
+                                          int score_cap = 0) {
   constexpr int VPL = Vpl<G>::value;
   const int half = lane >> 4, li = lane & 15;
   const uint4* K = reinterpret_cast<const uint4*>(stage);
@@ -142,6 +145,14 @@ __device__ __forceinline__ void page_step(const unsigned char* stage, const f2_t
   const int myk = li >> 1;
   const bool vis = row_visible(sp, lp * kPage + 2 * myk + half);
   rows_vis += __popc(__ballot_sync(0xffffffffu, vis) & 0x55555555u);
+  if constexpr (kScores) {
+#pragma unroll
+    for (int u = 0; u < VPL; ++u) {
+      const int gh = (G >= 2) ? ((li & 1) * (G / 2) + u) : 0;
+      if (vis && (G >= 2 || (li & 1) == 0))
+        scores[(size_t)gh * score_cap + lp * kPage + 2 * myk + half] = sc[u];
+    }
+  }
 
   float* pshare = ps;                 // [2 halves][8 rows][G]
   float* ashare = ps + 16 * G;        // [2 halves][G]
@@ -234,12 +245,13 @@ constexpr float kLazyMax = 8.f;
 // One page for G = 2 or 4. m_run[u], l_run[u] belong to head 2 tig + u (l_run: this lane's
 // tokens only; lanes with 2 tig >= G hold no head); acc is the half-warp P.V layout of
 // page_step.
-template <int G>
+template <int G, bool kScores = false>
 __device__ __forceinline__ void page_step_mma(const unsigned char* stage, const uint4 (&qv)[4],
                                               float scale_log2, float (&m_run)[2],
                                               float (&l_run)[2], f2_t (&acc)[G][4], float* ps,
                                               const SeqPlan& sp, int lp, int lane,
-                                              unsigned& rows_vis) {
+                                              unsigned& rows_vis, float* scores = nullptr,
+                                              int score_cap = 0) {
   static_assert(G == 4 || G == 2, "tensor-core scores serve two or four heads per KV head");
   const int gid = lane >> 2, tig = lane & 3;
   const unsigned char* k0 = stage + gid * kRowBytes + 16 * tig;
@@ -262,6 +274,14 @@ __device__ __forceinline__ void page_step_mma(const unsigned char* stage, const 
   for (int u = 0; u < 2; ++u) {
     s[0][u] = v0 ? c[u] * scale_log2 : -INFINITY;
     s[1][u] = v1 ? c[2 + u] * scale_log2 : -INFINITY;
+  }
+  if constexpr (kScores) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float* dst = scores + (size_t)(2 * tig + u) * score_cap + lp * kPage + gid;
+      if (head_ok && v0) dst[0] = s[0][u];
+      if (head_ok && v1) dst[8] = s[1][u];
+    }
   }
   float* pshare = ps;           // [2 halves][8 rows][G], as page_step
   float* ashare = ps + 16 * G;  // [G] rescale factors (written when a maximum is raised)
@@ -456,7 +476,7 @@ struct RingState {
 // reads q / k_new / v_new, the gate or writes global memory; it returns false (the same
 // answer in every thread of the CTA) when the launch is being abandoned, and the pass then
 // returns with rs.aborted set.
-template <int G, class Wait>
+template <int G, bool kScores = false, class Wait>
 __device__ __forceinline__ void decode_pass(const DecodeParams& p, const SplitSmem& sm,
                                             long long T, RingState& rs, Wait& dep_wait) {
   constexpr int VPL = MmaScores<G>::value ? 2 : Vpl<G>::value;  // softmax states per lane
@@ -607,10 +627,31 @@ __device__ __forceinline__ void decode_pass(const DecodeParams& p, const SplitSm
           fence_proxy_async_smem();  // this stage is refilled by a bulk copy later
           __syncwarp();
         }
-        if constexpr (MmaScores<G>::value)
-          page_step_mma<G>(st, qv, p.scale_log2, m_run, l_run, acc, ps, sp, r.lp, lane, rows_vis);
-        else
-          page_step<G>(st, q2, m_run, l_run, acc, ps, sp, r.lp, lane, rows_vis);
+        if constexpr (kScores) {
+          // Rows that are not visible may hold anything: a weight of zero times a NaN is a NaN.
+          bool hidden = false;
+          for (int row = 0; row < kPage; ++row) {
+            if (row_visible(sp, r.lp * kPage + row)) continue;
+            hidden = true;
+            *reinterpret_cast<uint2*>(st + kPageBytes + row * kRowBytes + 8 * lane) = make_uint2(0u, 0u);
+          }
+          if (hidden) {
+            fence_proxy_async_smem();  // this stage is refilled by a bulk copy later
+            __syncwarp();
+          }
+          float* scores = p.scores + ((size_t)b * p.hq + g * G) * p.score_cap;
+          if constexpr (MmaScores<G>::value)
+            page_step_mma<G, true>(st, qv, p.scale_log2, m_run, l_run, acc, ps, sp, r.lp, lane, rows_vis,
+                                   scores, p.score_cap);
+          else
+            page_step<G, true>(st, q2, m_run, l_run, acc, ps, sp, r.lp, lane, rows_vis, scores,
+                               p.score_cap);
+        } else {
+          if constexpr (MmaScores<G>::value)
+            page_step_mma<G>(st, qv, p.scale_log2, m_run, l_run, acc, ps, sp, r.lp, lane, rows_vis);
+          else
+            page_step<G>(st, q2, m_run, l_run, acc, ps, sp, r.lp, lane, rows_vis);
+        }
         ++pages_read;
       }
       __syncwarp();

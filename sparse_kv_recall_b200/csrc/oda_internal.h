@@ -43,6 +43,27 @@ int check_visibility(const oda_kv* kv, const oda_visibility* v);
 // oda_kv checks shared by every entry point (ODA_OK or an ODA_ERR_* code).
 int check_kv(const oda_kv* kv);
 
+// The other host checks of a decode call, after check_kv and check_visibility: heads, dtypes,
+// scale, commit, pointers and their alignment (everything but the workspace's size).
+int check_decode_args(const oda_kv* kv, const oda_visibility& vis, const void* q, int hq, float scale,
+                      const void* k_new, const void* v_new, const void* out, int out_dtype,
+                      const float* lse, const void* ws);
+
+// Decode launch that also stores the base-2 score of every visible position: scores fp32
+// [batch][hq][cap], the rest unwritten. Lets a dependent launch start early.
+int launch_decode_scores(const oda_kv* kv, const oda_visibility& vis, const void* q, int hq,
+                         float scale, const void* k_new, const void* v_new, void* out, int out_dtype,
+                         float* lse, float* scores, int cap, void* ws, size_t ws_bytes, void* stream);
+
+// 4-bit caches: the same page table and lengths as an oda_kv (its caches both point at the
+// codes), checks, workspace and launch of the decode kernel (scores nullable, as above).
+oda_kv kv4_as_kv(const oda_kv4* kv);
+int check_kv4(const oda_kv4* kv);
+int kv4_decode_ws_bytes(int batch, int hkv, int hq, size_t* bytes);
+int launch_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q, int hq,
+                      float scale, const void* k_new, const void* v_new, void* out, int out_dtype,
+                      float* lse, float* scores, int cap, void* ws, size_t ws_bytes, void* stream);
+
 // Decode workspace size and the offset of its merge tickets on the current device.
 int decode_ws_layout(int batch, int hkv, int hq, size_t* total, size_t* ticket_off);
 

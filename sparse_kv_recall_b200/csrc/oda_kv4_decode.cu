@@ -1,0 +1,807 @@
+// Decode attention over the 4-bit paged cache, under every visibility rule, split over the whole
+// GPU and merged inside the same launch (the work plan of the bf16 split kernel: equal contiguous
+// shares of the flattened (sequence, KV head, page) list, one online softmax per warp for all the
+// query heads of the KV head, the last CTA to arrive merges).
+//
+// Bound: a visible (position, KV head) row is 144 bytes instead of 512, so HBM leaves a warp a
+// third of the time per row; what competes with it is instruction issue, and within it the integer
+// pipe (half rate), which unpacks the codes. So both products run on the tensor cores straight from
+// codes, and scales and minima are applied to sums instead of to elements:
+//
+//   K:  s_p = sum_groups [ S_g sum_d (c - 8) q_d + (M_g + 8 S_g) sum_d q_d ]  (S, M of token p)
+//       mma.sync m16n8k16 fp16, A = 16 tokens x codes, B = columns (group, head) that hold q in the
+//       dims of their group and zero elsewhere, so one accumulator pair serves both groups.
+//   V:  o_d = sum_p (w_p S_g) (c - 7.5) + sum_p w_p (M_g + 7.5 S_g)
+//       A = codes as dims x 16 tokens, B = w_p S_g as a sum of two fp16 (columns (head, part): 22
+//       bits); the second sum has one term per token and group and runs on the CUDA cores.
+//
+// A code becomes an fp16 by one and-or that puts its nibble into the mantissa of 1024 (K) or 512
+// (V, one bit further up: 512 + c has room for the half) and one fp16 fma that subtracts the
+// offset; both are exact. Codes are centred so that the sums hold no offset to cancel: over a long
+// history the offset would grow with the token count, the signal only with its square root.
+// q is scaled by a power of two to the top of the fp16 range (bf16 has 8 significant bits, so every
+// dim within 2^-28 of the largest is exact), w S by a running power of two per head and group
+// that is raised when a weight passes 2^15.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "oda_decode.cuh"
+#include "oda_kv4.cuh"
+
+namespace oda {
+
+constexpr int kW4 = 8;               // warps per CTA
+constexpr int kThreads4 = kW4 * 32;
+constexpr int kSlots4 = 5;           // pages in flight per warp
+constexpr int kCtasPerSm4 = 2;
+constexpr int kMinShare4 = 8;        // units per CTA at least (one page per warp)
+constexpr int kPStride = 48;         // words per (page, head) of the weight exchange
+constexpr int kPWords = 4 * kPStride;
+
+struct Kv4Params {
+  PlanArgs plan;
+  unsigned char* cache;
+  int batch, hkv, hq;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_new;  // nullable: quantise into slot t and attend it there
+  const __nv_bfloat16* v_new;
+  float scale_log2;
+  void* out;
+  int out_bf16;
+  float* lse;
+  float* scores;               // [batch][hq][cap] base-2 scores of visible positions
+  int cap;
+  float* ws_o;
+  float* ws_lse;
+  unsigned int* ws_ticket;
+  int* status;
+  unsigned long long* stats;
+  unsigned long long wait_ns;
+  int test_stall;
+};
+
+__device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// (x & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(bits));
+  return d;
+}
+__device__ __forceinline__ uint32_t h2_pack(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float2 h2_unpack(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// Nibbles j of the two halves of w, as fp16 c - 8: j even in bits 0-3, odd in bits 4-7 of each
+// half of w (j < 2) or of w >> 8.
+__device__ __forceinline__ void k_codes(uint32_t w, uint32_t (&a)[4]) {
+  constexpr uint32_t kBase = 0x64006400u;  // 1024
+  const uint32_t w8 = w >> 8;
+  a[0] = h2_add(and_or(w, 0x000f000fu, kBase), 0xe408e408u);                // - 1032
+  a[1] = h2_fma(and_or(w, 0x00f000f0u, kBase), 0x2c002c00u, 0xd480d480u);   // / 16 - 72
+  a[2] = h2_add(and_or(w8, 0x000f000fu, kBase), 0xe408e408u);
+  a[3] = h2_fma(and_or(w8, 0x00f000f0u, kBase), 0x2c002c00u, 0xd480d480u);
+}
+// The same as c - 7.5, the nibbles one bit further up in the mantissa of 512.
+__device__ __forceinline__ void v_codes(uint32_t w, uint32_t (&a)[4]) {
+  constexpr uint32_t kBase = 0x60006000u;  // 512
+  const uint32_t w1 = w << 1, w7 = w >> 7;
+  a[0] = h2_add(and_or(w1, 0x001e001eu, kBase), 0xe00fe00fu);               // - 519.5
+  a[1] = h2_fma(and_or(w1, 0x01e001e0u, kBase), 0x2c002c00u, 0xd0f0d0f0u);  // / 16 - 39.5
+  a[2] = h2_add(and_or(w7, 0x001e001eu, kBase), 0xe00fe00fu);
+  a[3] = h2_fma(and_or(w7, 0x01e001e0u, kBase), 0x2c002c00u, 0xd0f0d0f0u);
+}
+
+// Lane roles. gid = lane / 4, tig = lane % 4. A step takes kPages pages. For the softmax a lane
+// holds two tokens, gid and gid + 8 of its page, of one head: with four heads per KV head the
+// columns are (group, head) and lanes tig, tig ^ 2 hold the two groups of a head pair; with two
+// (or one, the second idle) the columns are held twice, tig / 2 picks the page and tig ^ 1 is the
+// other group. For P.V a lane holds dims 64 g + 8 gid .. + 7 of both groups of head tig.
+template <int G>
+struct Roles {
+  static constexpr int kHeads = G == 4 ? 4 : 2;
+  static constexpr int kPages = G == 4 ? 1 : 2;
+  static constexpr int kOther = G == 4 ? 2 : 1;  // lane xor that holds the other group
+  __device__ static int group(int tig) { return (tig & kOther) ? 1 : 0; }
+  __device__ static int head(int tig) { return G == 4 ? 2 * (tig & 1) + (tig >> 1) : (tig & 1); }
+  __device__ static int page(int tig) { return G == 4 ? 0 : (tig >> 1); }
+  // tig of a lane whose softmax head is the P.V head of lane tig
+  __device__ static int owner(int tig) { return G == 4 ? ((tig >> 1) | ((tig & 1) << 1)) : (tig & 1); }
+};
+
+struct Kv4State {
+  float m, l;          // running maximum (base 2) and this lane's part of the softmax sum
+  float corr[2];       // this lane's part of sum w (M_g + 7.5 S_g)
+  float r[2];          // w S_g enters the tensor cores times this power of two
+  float acc[8][4];     // tile 4 g + j: dims 64 g + 8 gid + j (0, 1) and + j + 4 (2, 3); columns
+};                     // 2 tig, 2 tig + 1 are the two parts of head tig
+
+constexpr float kR0 = 1.2676506e30f;  // 2^100
+
+// The group's q as B fragments and per-column sums. Returns the power of two that undoes q's.
+template <int G>
+__device__ __forceinline__ float load_q4(const __nv_bfloat16* q, int lane, uint32_t (&b)[8][2],
+                                         float (&qs)[2]) {
+  using R = Roles<G>;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int grp = G == 4 ? gid >> 2 : (gid >> 1) & 1;
+  const int head = G == 4 ? gid & 3 : gid & 1;
+  float x[32];  // column gid's dims of this lane's 16-byte code chunk, in word order
+  float top = 0.f, sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (head < G && (e & 1) == grp)
+      v = *reinterpret_cast<const uint4*>(q + head * kHeadDim + 64 * (e & 1) + 8 * (2 * tig + (e >> 1)));
+    float f[8];
+    unpack8(v, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[8 * e + k] = f[k];
+      top = fmaxf(top, fabsf(f[k]));
+      sum += f[k];
+    }
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  qs[0] = __shfl_sync(0xffffffffu, sum, 8 * tig);
+  qs[1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4);
+  const uint32_t ebits = __reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23;
+  const uint32_t f = min(268u - min(ebits, 254u), 253u);  // largest |q| to [2^14, 2^15)
+  const float up = __uint_as_float(f << 23);
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const int e = s >> 1, j = 2 * (s & 1);
+    b[s][0] = h2_pack(x[8 * e + j] * up, x[8 * e + j + 4] * up);
+    b[s][1] = h2_pack(x[8 * e + j + 1] * up, x[8 * e + j + 5] * up);
+  }
+  return __uint_as_float((254u - f) << 23);
+}
+
+struct PageView {
+  const unsigned char* st;  // the page in shared memory (any page's, if this one is not there)
+  int pos;                  // its first position
+  bool ok;                  // it was read
+};
+
+// Visible rows among the 16 positions from `pos`.
+__device__ __forceinline__ int rows_in_page(const SeqPlan& s, int pos) {
+  const int lo = max(s.row_lo, pos), hi = min(s.row_hi, pos + kPage - 1);
+  const int glo = max(lo, s.gap_lo), ghi = min(hi, s.gap_hi - 1);
+  return max(0, hi - lo + 1) - max(0, ghi - glo + 1);
+}
+
+// One step: kPages pages. kq undoes q's power of two and carries the softmax scale in base 2;
+// qs is sum q times that scale.
+template <int G, bool kScores>
+__device__ __forceinline__ void kv4_step(const PageView (&pg)[Roles<G>::kPages], bool all_visible,
+                                         const SeqPlan& sp, const uint32_t (&qb)[8][2], float kq,
+                                         const float (&qs)[2], Kv4State& st, uint32_t* pw,
+                                         float* scores, int cap, int lane) {
+  using R = Roles<G>;
+  constexpr int NP = R::kPages, HG = R::kHeads;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int mygrp = R::group(tig), myhead = R::head(tig), mypage = R::page(tig);
+
+  // ---- scores: c[page][token gid: 0, 1; gid + 8: 2, 3][columns 2 tig, 2 tig + 1] ----
+  float c[NP][4];
+#pragma unroll
+  for (int n = 0; n < NP; ++n) {
+    const uint4 wa = *reinterpret_cast<const uint4*>(pg[n].st + gid * kKv4RowBytes + 16 * tig);
+    const uint4 wb = *reinterpret_cast<const uint4*>(pg[n].st + (gid + 8) * kKv4RowBytes + 16 * tig);
+    const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t ca[4], cb[4];
+      k_codes(a[e], ca);
+      k_codes(b[e], cb);
+      mma_16816_f16(c[n], ca[0], cb[0], ca[1], cb[1], qb[2 * e][0], qb[2 * e][1]);
+      mma_16816_f16(c[n], ca[2], cb[2], ca[3], cb[3], qb[2 * e + 1][0], qb[2 * e + 1][1]);
+    }
+  }
+  const PageView& my = (NP == 2 && mypage) ? pg[NP - 1] : pg[0];
+  const uint4 ma = *reinterpret_cast<const uint4*>(my.st + kKv4MetaOff + gid * kKv4MetaBytes);
+  const uint4 mb = *reinterpret_cast<const uint4*>(my.st + kKv4MetaOff + (gid + 8) * kKv4MetaBytes);
+  float cc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) cc[i] = (NP == 2 && mypage) ? c[NP - 1][i] : c[0][i];
+  const uint32_t ka = mygrp ? ma.y : ma.x, kb = mygrp ? mb.y : mb.x;
+  const float sa = kv4_scale(ka), sb = kv4_scale(kb);
+  const float za = fmaf(8.f, sa, kv4_min(ka)), zb = fmaf(8.f, sb, kv4_min(kb));
+  const float s00 = fmaf(sa * kq, cc[0], za * qs[0]), s01 = fmaf(sa * kq, cc[1], za * qs[1]);
+  const float s10 = fmaf(sb * kq, cc[2], zb * qs[0]), s11 = fmaf(sb * kq, cc[3], zb * qs[1]);
+  // keep the head this lane owns, trade the other's partial sums for the missing group's
+  float x0 = (mygrp ? s01 : s00) + __shfl_xor_sync(0xffffffffu, mygrp ? s00 : s01, R::kOther);
+  float x1 = (mygrp ? s11 : s10) + __shfl_xor_sync(0xffffffffu, mygrp ? s10 : s11, R::kOther);
+
+  bool v0 = true, v1 = true;
+  if (!all_visible) {
+    v0 = my.ok && row_visible(sp, my.pos + gid);
+    v1 = my.ok && row_visible(sp, my.pos + gid + 8);
+  }
+  if constexpr (kScores) {
+    if (myhead < G) {
+      float* dst = scores + (size_t)myhead * cap + my.pos;
+      if (v0) dst[gid] = x0;
+      if (v1) dst[gid + 8] = x1;
+    }
+  }
+  x0 = v0 ? x0 : -INFINITY;
+  x1 = v1 ? x1 : -INFINITY;
+
+  // ---- online softmax; the maximum is raised only when a score passes it by 2^kLazyMax ----
+  if (__any_sync(0xffffffffu, fmaxf(x0, x1) > st.m + kLazyMax)) {
+    float mx = fmaxf(x0, x1);
+    if (NP == 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    const bool up = mx > st.m + kLazyMax;
+    const float al = !up ? 1.f : (st.m == -INFINITY ? 0.f : ex2_fast(st.m - mx));
+    if (up) st.m = mx;
+    st.l *= al;
+    st.corr[0] *= al;
+    st.corr[1] *= al;
+    const float ah = __shfl_sync(0xffffffffu, al, (lane & ~3) | R::owner(tig));
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st.acc[t][i] *= ah;
+  }
+  const float p0 = x0 == -INFINITY ? 0.f : ex2_fast(x0 - st.m);
+  const float p1 = x1 == -INFINITY ? 0.f : ex2_fast(x1 - st.m);
+  st.l += p0 + p1;
+
+  // ---- weights times the V scales, as two fp16 each ----
+  const uint32_t va[2] = {v0 ? ma.z : 0u, v0 ? ma.w : 0u}, vb[2] = {v1 ? mb.z : 0u, v1 ? mb.w : 0u};
+  float y0[2], y1[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float s0 = kv4_scale(va[g]), s1 = kv4_scale(vb[g]);
+    st.corr[g] = fmaf(p0, fmaf(7.5f, s0, kv4_min(va[g])), st.corr[g]);
+    st.corr[g] = fmaf(p1, fmaf(7.5f, s1, kv4_min(vb[g])), st.corr[g]);
+    y0[g] = p0 * s0;
+    y1[g] = p1 * s1;
+  }
+  bool high = false;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) high |= fmaxf(y0[g], y1[g]) * st.r[g] > 32768.f;
+  if (__any_sync(0xffffffffu, high)) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float ym = fmaxf(y0[g], y1[g]);
+      if (NP == 2) ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 2));
+      ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 4));
+      ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 8));
+      ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 16));
+      float ratio = 1.f;
+      if (ym * st.r[g] > 32768.f) {  // the largest weight to [2^7, 2^8)
+        const float rn = __uint_as_float((261u - min(__float_as_uint(ym) >> 23, 254u)) << 23);
+        ratio = rn / st.r[g];
+        st.r[g] = rn;
+      }
+      const float rh = __shfl_sync(0xffffffffu, ratio, (lane & ~3) | R::owner(tig));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.acc[4 * g + j][i] *= rh;
+    }
+  }
+  uint32_t hi[2], lo[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float w0 = y0[g] * st.r[g], w1 = y1[g] * st.r[g];
+    hi[g] = h2_pack(w0, w1);
+    const float2 f = h2_unpack(hi[g]);
+    lo[g] = h2_pack(w0 - f.x, w1 - f.y);
+  }
+  *reinterpret_cast<uint4*>(pw + (mypage * HG + myhead) * kPStride + 4 * gid) =
+      make_uint4(hi[0], hi[1], lo[0], lo[1]);
+  __syncwarp();
+
+  // ---- P.V ----
+  const int bh = (gid >> 1) & (HG - 1), part = gid & 1;
+#pragma unroll
+  for (int n = 0; n < NP; ++n) {
+    const uint32_t* src = pw + (n * HG + bh) * kPStride + 2 * part;
+    const uint2 b0 = *reinterpret_cast<const uint2*>(src + 4 * tig);
+    const uint2 b1 = *reinterpret_cast<const uint2*>(src + 4 * (tig + 4));
+    const unsigned char* vs = pg[n].st + kKv4VOff + tig * kKv4RowBytes + 8 * gid;
+    const uint2 w0 = *reinterpret_cast<const uint2*>(vs);
+    const uint2 w1 = *reinterpret_cast<const uint2*>(vs + 8 * kKv4RowBytes);
+    const uint2 w2 = *reinterpret_cast<const uint2*>(vs + 4 * kKv4RowBytes);
+    const uint2 w3 = *reinterpret_cast<const uint2*>(vs + 12 * kKv4RowBytes);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint32_t u0 = g ? w0.y : w0.x, u1 = g ? w1.y : w1.x;
+      const uint32_t u2 = g ? w2.y : w2.x, u3 = g ? w3.y : w3.x;
+      uint32_t a0[4], a1[4], a2[4], a3[4];
+      v_codes(__byte_perm(u0, u1, 0x5410), a0);
+      v_codes(__byte_perm(u0, u1, 0x7632), a1);
+      v_codes(__byte_perm(u2, u3, 0x5410), a2);
+      v_codes(__byte_perm(u2, u3, 0x7632), a3);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        mma_16816_f16(st.acc[4 * g + j], a0[j], a1[j], a2[j], a3[j], g ? b0.y : b0.x, g ? b1.y : b1.x);
+    }
+  }
+  __syncwarp();  // the exchange area is written again by the next step
+}
+
+__device__ __forceinline__ void kv4_write(const Kv4Params& p, int b, int h, int dim, float o, float l2) {
+  const size_t row = (size_t)b * p.hq + h;
+  if (p.out_bf16)
+    static_cast<__nv_bfloat16*>(p.out)[row * kHeadDim + dim] = __float2bfloat16_rn(o);
+  else
+    static_cast<float*>(p.out)[row * kHeadDim + dim] = o;
+  if (p.lse != nullptr && dim == 0)
+    p.lse[row] = l2 == -INFINITY ? -INFINITY : l2 * 0.69314718055994531f;
+}
+
+struct Kv4Smem {
+  static constexpr int kSlotsOff = 0;
+  static constexpr int kBarsOff = kW4 * kSlots4 * kKv4PageBytes;
+  static constexpr int kPOff = kBarsOff + (kW4 * kSlots4 * 8 + 15) / 16 * 16;
+  static constexpr int kPreOff = kPOff + kW4 * kPWords * 4;
+  static constexpr int kBytes = kPreOff + (kMaxBatch + 1) * 4;
+};
+
+template <int G, bool kScores>
+__global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(const Kv4Params p) {
+  using R = Roles<G>;
+  constexpr int NP = R::kPages, HG = R::kHeads;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int s_align, s_last;
+  __shared__ unsigned long long s_rows, s_pages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  unsigned char* slots = smem + Kv4Smem::kSlotsOff + warp * kSlots4 * kKv4PageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Kv4Smem::kBarsOff) + warp * kSlots4;
+  uint32_t* pw = reinterpret_cast<uint32_t*>(smem + Kv4Smem::kPOff) + warp * kPWords;
+  int* pre = reinterpret_cast<int*>(smem + Kv4Smem::kPreOff);
+  const int B = p.batch, Hkv = p.hkv;
+  const int P = gridDim.x, cta = blockIdx.x;
+
+  // ---- prefix of visible units per sequence, share alignment ----
+  if (lane == 0) {
+    for (int s = 0; s < kSlots4; ++s) mbar_init(&bars[s], 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) {
+    s_rows = 0;
+    s_pages = 0;
+    pre[0] = 0;
+  }
+  for (int b = tid; b < B; b += kThreads4) {
+    const SeqPlan sp = make_plan(p.plan, b);
+    pre[b + 1] = sp.npages * Hkv;
+    if (cta == 0 && sp.err != 0) report(p.status, sp.err);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int carry = 0;
+    unsigned vmin = 0xffffffffu, vmax = 0u, active = 0u;
+    for (int base = 0; base < B; base += 32) {
+      const int i = base + lane;
+      int v = i < B ? pre[i + 1] : 0;
+      const unsigned nz = v > 0 ? (unsigned)v : 0u;
+      vmin = min(vmin, __reduce_min_sync(0xffffffffu, nz ? nz : 0xffffffffu));
+      vmax = max(vmax, __reduce_max_sync(0xffffffffu, nz));
+      active += __popc(__ballot_sync(0xffffffffu, nz != 0u));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += n;
+      }
+      v += carry;
+      if (i < B) pre[i + 1] = v;
+      carry = __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) s_align = (active > 0 && vmin == vmax) ? (int)active * Hkv : 0;
+  }
+  __syncthreads();
+  const long long T = pre[B];
+  if constexpr (kScores) griddep_launch_dependents();
+
+  // Equal contiguous shares; with equal page counts the CTA count is a multiple of the non-empty
+  // (sequence, KV head) pairs, so that every share falls inside one of them.
+  int Pe = (int)min((long long)P, (T + kMinShare4 - 1) / kMinShare4);
+  if (s_align > 0) {
+    const int up = (Pe + s_align - 1) / s_align * s_align;
+    if (up <= P) Pe = up;
+    else if (Pe >= s_align) Pe -= Pe % s_align;
+  }
+  const uint64_t policy = l2_evict_first_policy();
+  unsigned wcount = 0;
+  bool dead = false;
+  long long x = cta < Pe ? (T * cta) / Pe : 0;
+  const long long x_end = cta < Pe ? (T * (cta + 1)) / Pe : 0;
+  while (x < x_end) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    const int b = lo;
+    const int npg = (pre[b + 1] - pre[b]) / Hkv;
+    const long long off = x - pre[b];
+    const int g = (int)(off / npg);
+    const int j0 = (int)(off - (long long)g * npg);
+    const long long seg0 = pre[b] + (long long)g * npg, seg1 = seg0 + npg;
+    const long long xe = min(x_end, seg1);
+    const int j1 = j0 + (int)(xe - x);
+    const SeqPlan sp = make_plan(p.plan, b);
+    const int bg = b * Hkv + g;
+
+    // this warp's pages: runs of NP consecutive list entries, strided over the warps
+    const int steps = (j1 - j0 + NP - 1) / NP;
+    const int my_steps = steps > warp ? (steps - warp + kW4 - 1) / kW4 : 0;
+    const int cnt = my_steps * NP;  // page n of this warp: entry j0 + (n / NP * kW4 + warp) * NP + n % NP
+    auto entry = [&](int n) { return j0 + ((n / NP) * kW4 + warp) * NP + n % NP; };
+    auto ref_of = [&](int n) {
+      PageRef r;
+      r.lp = 0;
+      r.pb = 0;
+      r.err = -1;  // past the share's end
+      const int j = n < cnt ? entry(n) : j1;
+      return j < j1 ? page_ref(p.plan, sp, b, j) : r;
+    };
+    auto issue = [&](int n) {  // lane 0: bring page n into its slot
+      const PageRef r = ref_of(n);
+      const unsigned k = wcount + n;
+      uint64_t* bar = &bars[k % kSlots4];
+      if (p.test_stall == 1 && cta == 0 && warp == 0 && k == 0) {
+        mbar_arrive_expect_tx(bar, 16u);  // test hook: bytes that never arrive
+      } else if (r.err == 0) {
+        mbar_arrive_expect_tx(bar, kKv4PageBytes);
+        bulk_load(slots + (k % kSlots4) * kKv4PageBytes,
+                  p.cache + ((size_t)r.pb * Hkv + g) * kKv4PageBytes, kKv4PageBytes, bar, policy);
+      } else {
+        if (r.err > 0) report(p.status, r.err);
+        mbar_arrive(bar);
+      }
+    };
+    if (!dead && lane == 0)
+      for (int n = 0; n < min(cnt, kSlots4); ++n) issue(n);
+    __syncwarp();
+
+    uint32_t qb[8][2];
+    float qs[2];
+    float kq = load_q4<G>(p.q + ((size_t)b * p.hq + g * G) * kHeadDim, lane, qb, qs) * p.scale_log2;
+    qs[0] *= p.scale_log2;
+    qs[1] *= p.scale_log2;
+    float* scores = nullptr;
+    if constexpr (kScores) scores = p.scores + ((size_t)b * p.hq + g * G) * p.cap;
+
+    Kv4State st;
+    st.m = -INFINITY;
+    st.l = 0.f;
+    st.corr[0] = st.corr[1] = 0.f;
+    st.r[0] = st.r[1] = kR0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st.acc[t][i] = 0.f;
+    unsigned rows_vis = 0, pages_read = 0;
+
+    for (int n = 0; n < cnt && !dead; n += NP) {
+      PageView pg[NP];
+      bool all_visible = true;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const unsigned k = wcount + n + i;
+        const PageRef r = ref_of(n + i);
+        unsigned char* slot = slots + (k % kSlots4) * kKv4PageBytes;
+        if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bars[k % kSlots4], (k / kSlots4) & 1u, p.wait_ns))) {
+          if (lane == 0) report(p.status, ODA_DEV_TIMEOUT);
+          // let the copies already started into the other slots land, then stop
+          for (int m = n + i + 1; m < min(cnt, n + kSlots4); ++m)
+            mbar_wait(&bars[(wcount + m) % kSlots4], ((wcount + m) / kSlots4) & 1u, p.wait_ns);
+          dead = true;
+        }
+        pg[i].st = slot;
+        pg[i].pos = r.lp * kPage;
+        pg[i].ok = r.err == 0;
+        if (pg[i].ok && !dead) {
+          if (p.k_new != nullptr && r.lp == sp.t / kPage) {
+            // commit: the step's K/V, quantised, take slot t in the cache and in this copy
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                (lane < 16 ? p.k_new : p.v_new) + (size_t)bg * kHeadDim + 8 * (lane & 15));
+            uint32_t meta;
+            const uint32_t word = kv4_quantise(v, lane, meta);
+            kv4_store_row(slot, sp.t % kPage, word, meta, lane);
+            kv4_store_row(p.cache + ((size_t)r.pb * Hkv + g) * kKv4PageBytes, sp.t % kPage, word, meta, lane);
+            fence_proxy_async_smem();  // this slot is refilled by a bulk copy later
+            __syncwarp();
+          }
+          const int rows = rows_in_page(sp, pg[i].pos);
+          rows_vis += rows;
+          ++pages_read;
+          all_visible &= rows == kPage;
+        } else {
+          all_visible = false;
+        }
+      }
+      if (dead) break;
+      kv4_step<G, kScores>(pg, all_visible, sp, qb, kq, qs, st, pw, scores, p.cap, lane);
+      if (lane == 0)
+        for (int i = 0; i < NP; ++i)
+          if (n + i + kSlots4 < cnt) issue(n + i + kSlots4);
+      __syncwarp();
+    }
+    wcount += cnt;
+
+    // ---- merge the CTA's warps ----
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) {
+      st.l += __shfl_xor_sync(0xffffffffu, st.l, o);
+      st.corr[0] += __shfl_xor_sync(0xffffffffu, st.corr[0], o);
+      st.corr[1] += __shfl_xor_sync(0xffffffffu, st.corr[1], o);
+    }
+    if (NP == 2) {
+      st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
+      st.corr[0] += __shfl_xor_sync(0xffffffffu, st.corr[0], 2);
+      st.corr[1] += __shfl_xor_sync(0xffffffffu, st.corr[1], 2);
+    }
+    if (p.stats != nullptr && lane == 0 && (rows_vis | pages_read)) {
+      atomicAdd(&s_rows, (unsigned long long)rows_vis);
+      atomicAdd(&s_pages, (unsigned long long)pages_read);
+    }
+    __syncthreads();  // every warp is done with its slots: reuse them as merge scratch
+    if (p.stats != nullptr && tid == 0) {
+      if (s_rows) atomicAdd(&p.stats[ODA_STAT_ROWS], s_rows);
+      if (s_pages) atomicAdd(&p.stats[ODA_STAT_PAGES], s_pages);
+      s_rows = 0;
+      s_pages = 0;
+    }
+    float* Mw = reinterpret_cast<float*>(smem);  // [kW4][HG]
+    float* Lw = Mw + kW4 * HG;                   // [kW4][HG]
+    float* Aw = Lw + kW4 * HG;                   // [kW4][HG][128]
+    if (gid == 0 && (NP == 1 || tig < 2)) {
+      Mw[warp * HG + R::head(tig)] = st.m;
+      Lw[warp * HG + R::head(tig)] = st.l;
+    }
+    {
+      const int src = (lane & ~3) | R::owner(tig);
+      float corr[2], inv[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        corr[i] = __shfl_sync(0xffffffffu, st.corr[i], src);
+        inv[i] = 1.f / __shfl_sync(0xffffffffu, st.r[i], src);
+      }
+      if (tig < HG) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float o[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[j] = fmaf(st.acc[4 * i + j][0] + st.acc[4 * i + j][1], inv[i], corr[i]);
+            o[j + 4] = fmaf(st.acc[4 * i + j][2] + st.acc[4 * i + j][3], inv[i], corr[i]);
+          }
+          float4* dst = reinterpret_cast<float4*>(Aw + (warp * HG + tig) * kHeadDim + 64 * i + 8 * gid);
+          dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+          dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+        }
+      }
+    }
+    __syncthreads();
+    const int c_first = cta_of(seg0, T, Pe);
+    const int n_contrib = cta_of(seg1 - 1, T, Pe) - c_first + 1;
+    const size_t slot = (size_t)cta + bg;
+    for (int e = tid; e < G * kHeadDim; e += kThreads4) {
+      const int h = e / kHeadDim, dim = e % kHeadDim;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kW4; ++w) M = fmaxf(M, Mw[w * HG + h]);
+      float o = 0.f, l2 = -INFINITY;
+      if (M != -INFINITY) {
+        float L = 0.f, a = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW4; ++w) {
+          const float ms = Mw[w * HG + h];
+          const float f = ms == -INFINITY ? 0.f : ex2_fast(ms - M);
+          L = fmaf(f, Lw[w * HG + h], L);
+          a = fmaf(f, Aw[(w * HG + h) * kHeadDim + dim], a);
+        }
+        o = a / L;
+        l2 = M + log2f(L);
+      }
+      if (n_contrib == 1) {
+        kv4_write(p, b, g * G + h, dim, o, l2);
+      } else {
+        p.ws_o[(slot * G + h) * kHeadDim + dim] = o;
+        if (dim == 0) p.ws_lse[slot * G + h] = l2;
+      }
+    }
+    if (n_contrib > 1) {
+      __syncthreads();  // the CTA's partial is written; thread 0 publishes it (release)
+      if (tid == 0) s_last = ticket_arrive(&p.ws_ticket[bg]) == (unsigned)(n_contrib - 1);
+      __syncthreads();  // ... and the last CTA's thread 0 acquired everyone's partials
+      if (s_last) {
+        const size_t s0 = (size_t)c_first + bg;
+        float* sw = reinterpret_cast<float*>(smem);  // [n_contrib][G] log-sums, then weights
+        for (int i = tid; i < n_contrib * G; i += kThreads4) sw[i] = __ldcg(&p.ws_lse[s0 * G + i]);
+        __shared__ float s_max[4], s_sum[4];
+        __syncthreads();
+        if (warp < G) {
+          float m = -INFINITY, sum = 0.f;
+          for (int s = lane; s < n_contrib; s += 32) m = fmaxf(m, sw[s * G + warp]);
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          for (int s = lane; s < n_contrib; s += 32) {
+            const float ls = sw[s * G + warp];
+            const float w = ls == -INFINITY ? 0.f : ex2_fast(ls - m);
+            sw[s * G + warp] = w;
+            sum += w;
+          }
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) {
+            s_max[warp] = m;
+            s_sum[warp] = sum;
+          }
+        }
+        __syncthreads();
+        for (int e = tid; e < G * kHeadDim; e += kThreads4) {
+          const int h = e / kHeadDim, dim = e % kHeadDim;
+          float a = 0.f;
+          for (int s = 0; s < n_contrib; ++s)
+            a = fmaf(sw[s * G + h], __ldcg(&p.ws_o[((s0 + s) * G + h) * kHeadDim + dim]), a);
+          const float M = s_max[h], L = s_sum[h];
+          const bool none = M == -INFINITY;
+          kv4_write(p, b, g * G + h, dim, none ? 0.f : a / L, none ? -INFINITY : M + log2f(L));
+        }
+        if (tid == 0) p.ws_ticket[bg] = 0u;  // leave the workspace zeroed
+      }
+    }
+    fence_proxy_async_smem();  // merge scratch is the next piece's slot memory
+    __syncthreads();
+    x = xe;
+  }
+
+  // Sequences with nothing visible (bad length, empty keep list) but not gated off.
+  for (int i = cta; i < B * Hkv; i += P) {
+    const int b = i / Hkv;
+    if (pre[b + 1] == pre[b] && !(p.plan.gate != nullptr && p.plan.gate[b] == 0))
+      for (int e = tid; e < G * kHeadDim; e += kThreads4)
+        kv4_write(p, b, (i % Hkv) * G + e / kHeadDim, e % kHeadDim, 0.f, -INFINITY);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------------------
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Kv4Ws {
+  size_t lse_off, ticket_off, total;
+};
+
+static Kv4Ws kv4_ws(int batch, int hkv, int G, int sms) {
+  const size_t slots = (size_t)sms * kCtasPerSm4 + (size_t)batch * hkv;
+  Kv4Ws w;
+  w.lse_off = up256(slots * G * kHeadDim * sizeof(float));
+  w.ticket_off = w.lse_off + up256(slots * G * sizeof(float));
+  w.total = w.ticket_off + up256((size_t)batch * hkv * sizeof(unsigned));
+  return w;
+}
+
+int kv4_decode_ws_bytes(int batch, int hkv, int hq, size_t* bytes) {
+  if (bytes == nullptr || batch < 0 || hkv < 1 || hq < 1) return ODA_ERR_INVALID_ARG;
+  const int G = hq / hkv;
+  if (hq % hkv != 0 || (G != 1 && G != 2 && G != 4)) return ODA_ERR_UNSUPPORTED_SHAPE;
+  DeviceInfo di;
+  const int rc = current_device_info(&di);
+  if (rc != ODA_OK) return rc;
+  *bytes = kv4_ws(batch, hkv, G, di.sms).total;
+  return ODA_OK;
+}
+
+template <int G, bool kScores>
+static int launch_kv4(const Kv4Params& p, const DeviceInfo& di, cudaStream_t st) {
+  static bool done[64] = {false};
+  if (di.device < 0 || di.device >= 64) return ODA_ERR_CUDA;
+  if (!done[di.device]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kv4_decode_kernel<G, kScores>, cudaFuncAttributeMaxDynamicSharedMemorySize, Kv4Smem::kBytes);
+    if (e != cudaSuccess) return cuda_status(e);
+    done[di.device] = true;
+  }
+  kv4_decode_kernel<G, kScores><<<di.sms * kCtasPerSm4, kThreads4, Kv4Smem::kBytes, st>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+int launch_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q, int hq,
+                      float scale, const void* k_new, const void* v_new, void* out, int out_dtype,
+                      float* lse, float* scores, int cap, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_kv4(kv);
+  if (rc != ODA_OK) return rc;
+  const oda_kv k = kv4_as_kv(kv);
+  if ((rc = check_visibility(&k, vis)) != ODA_OK) return rc;
+  size_t need = 0;
+  if ((rc = check_decode_args(&k, *vis, q, hq, scale, k_new, v_new, out, out_dtype, lse, ws)) != ODA_OK)
+    return rc;
+  if (kv->batch == 0) return ODA_OK;
+  if ((rc = kv4_decode_ws_bytes(kv->batch, kv->num_kv_heads, hq, &need)) != ODA_OK) return rc;
+  if (ws_bytes < need) return ODA_ERR_WORKSPACE_TOO_SMALL;
+  DeviceInfo di;
+  if ((rc = current_device_info(&di)) != ODA_OK) return rc;
+  const int G = hq / kv->num_kv_heads;
+  const Kv4Ws wl = kv4_ws(kv->batch, kv->num_kv_heads, G, di.sms);
+  Kv4Params p;
+  p.plan = plan_args(&k, *vis);
+  p.cache = static_cast<unsigned char*>(kv->cache);
+  p.batch = kv->batch;
+  p.hkv = kv->num_kv_heads;
+  p.hq = hq;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = out;
+  p.out_bf16 = out_dtype == ODA_BF16;
+  p.lse = lse;
+  p.scores = scores;
+  p.cap = cap;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  p.ws_o = reinterpret_cast<float*>(w);
+  p.ws_lse = reinterpret_cast<float*>(w + wl.lse_off);
+  p.ws_ticket = reinterpret_cast<unsigned*>(w + wl.ticket_off);
+  p.status = kv->dev_status;
+  p.stats = kv->stats;
+  p.wait_ns = test_wait_ns();
+  p.test_stall = test_stall() == ODA_STALL_DECODE_RING ? 1 : 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (scores != nullptr) {
+    switch (G) {
+      case 1: return launch_kv4<1, true>(p, di, st);
+      case 2: return launch_kv4<2, true>(p, di, st);
+      default: return launch_kv4<4, true>(p, di, st);
+    }
+  }
+  switch (G) {
+    case 1: return launch_kv4<1, false>(p, di, st);
+    case 2: return launch_kv4<2, false>(p, di, st);
+    default: return launch_kv4<4, false>(p, di, st);
+  }
+}
+
+}  // namespace oda
+
+using namespace oda;
+
+extern "C" int oda_kv4_decode_workspace_size(int32_t batch, int32_t num_kv_heads,
+                                             int32_t num_q_heads, size_t* bytes) {
+  return kv4_decode_ws_bytes(batch, num_kv_heads, num_q_heads, bytes);
+}
+
+extern "C" int oda_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q,
+                              int32_t num_q_heads, float scale, const void* k_new,
+                              const void* v_new, void* out, int32_t out_dtype, float* lse, void* ws,
+                              size_t ws_bytes, void* stream) {
+  return launch_kv4_decode(kv, vis, q, num_q_heads, scale, k_new, v_new, out, out_dtype, lse, nullptr,
+                           0, ws, ws_bytes, stream);
+}

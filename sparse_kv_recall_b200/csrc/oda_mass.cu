@@ -1,0 +1,223 @@
+// Decode attention that also accumulates the attention weight of every cached position: what
+// eviction from the cache goes by (oda_evict.cu).
+//
+// A position's weight is 2^(s - lse) with the log-sum of the whole visible set, which is known only
+// when the decode kernel's last merge is done. So the decode kernel leaves every visible position's
+// score in the workspace (4 bytes a query head, where recomputing it would read the K row again:
+// 256 bytes in bf16, 72 in 4 bits) and a second kernel, launched with a programmatic dependency,
+// turns scores into weights and adds them up over the query heads of the KV head. Bound: memory,
+// 4 G + 8 bytes per position and KV head, the scores mostly out of L2.
+#include <math.h>
+
+#include "oda_decode.cuh"
+#include "oda_internal.h"
+#include "oda_plan.cuh"
+
+namespace oda {
+
+constexpr int kMassThreads = 256;
+
+struct MassParams {
+  PlanArgs plan;
+  int hkv, hq, group;
+  const float* scores;   // [batch][hq][cap], base 2
+  int cap;
+  const float* lse;      // [batch][hq], natural
+  const float* mass_in;  // nullable (zero); may be mass_out
+  float* mass_out;       // [batch][hkv][mass_tokens]
+  long long mass_tokens;
+  int blocks_per_row;
+};
+
+// Whether logical page lp is in the sequence's list.
+__device__ __forceinline__ bool page_listed(const PlanArgs& a, const SeqPlan& s, int b, int lp) {
+  if (a.mode != ODA_MODE_KEEP) {
+#pragma unroll
+    for (int i = 0; i < kMaxRuns; ++i)
+      if (lp >= run_first(s, i) && lp < run_first(s, i) + run_len(s, i)) return true;
+    return false;
+  }
+  const int32_t* kb = a.keep_blocks + (size_t)b * a.max_keep;
+  int lo = 0, hi = s.npages;  // first entry >= lp
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (kb[mid] < lp) lo = mid + 1; else hi = mid;
+  }
+  return lo < s.npages && kb[lo] == lp;
+}
+
+// Four consecutive positions a thread. kAlias (mass_out is mass_in): only listed pages are
+// touched; otherwise every position of the sequence is written.
+template <bool kAlias>
+__global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassParams p) {
+  griddep_wait();
+  const int bg = blockIdx.x / p.blocks_per_row;
+  const int b = bg / p.hkv, g = bg % p.hkv;
+  const SeqPlan sp = make_plan(p.plan, b);
+  if (sp.skip || sp.err != 0) return;
+  int idx = ((blockIdx.x % p.blocks_per_row) * kMassThreads + threadIdx.x) * 4;
+  bool listed = true;
+  if (kAlias) {
+    if (idx >= sp.npages * kPage) return;
+    const PageRef r = page_ref(p.plan, sp, b, idx / kPage);
+    if (r.err != 0) return;
+    idx = r.lp * kPage + idx % kPage;
+  } else {
+    if (idx > sp.t) return;
+    listed = page_listed(p.plan, sp, b, idx / kPage);
+    if (listed) {
+      const int pb = p.plan.block_table[(size_t)b * p.plan.max_blocks + idx / kPage];
+      listed = pb >= 0 && pb < p.plan.num_blocks;  // a bad page was not attended
+    }
+  }
+  bool vis[4];
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= vis[i] = listed && row_visible(sp, idx + i);
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  if (any) {
+    for (int h = 0; h < p.group; ++h) {
+      const size_t row = (size_t)b * p.hq + g * p.group + h;
+      const float4 s4 = *reinterpret_cast<const float4*>(p.scores + row * p.cap + idx);
+      const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+      const float l = p.lse[row];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (vis[i])  // (the difference in natural units first: it is small where the weight is not)
+          w[i] += ex2_fast(fmaf(s[i], 0.69314718055994531f, -l) * 1.4426950408889634f);
+    }
+  }
+  const size_t at = (size_t)bg * p.mass_tokens + idx;
+  float in[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.mass_in != nullptr) {
+    const float4 v = *reinterpret_cast<const float4*>(p.mass_in + at);
+    in[0] = v.x; in[1] = v.y; in[2] = v.z; in[3] = v.w;
+  }
+  if (idx + 3 <= sp.t) {
+    *reinterpret_cast<float4*>(p.mass_out + at) =
+        make_float4(in[0] + w[0], in[1] + w[1], in[2] + w[2], in[3] + w[3]);
+  } else {
+    for (int i = 0; i < 4 && idx + i <= sp.t; ++i) p.mass_out[at + i] = in[i] + w[i];
+  }
+}
+
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace: the decode call's, a log-sum per query head, the scores.
+static int mass_ws(int batch, int hkv, int hq, int max_blocks, bool kv4, size_t* decode, size_t* lse_off,
+                   size_t* scores_off, size_t* total) {
+  if (batch < 0 || hkv < 1 || hq < 1 || max_blocks < 1) return ODA_ERR_INVALID_ARG;
+  int rc;
+  if (kv4) {
+    rc = kv4_decode_ws_bytes(batch, hkv, hq, decode);
+  } else {
+    size_t ticket = 0;
+    rc = hq % hkv != 0 || (hq / hkv != 1 && hq / hkv != 2 && hq / hkv != 4)
+             ? ODA_ERR_UNSUPPORTED_SHAPE
+             : decode_ws_layout(batch, hkv, hq, decode, &ticket);
+  }
+  if (rc != ODA_OK) return rc;
+  *lse_off = up256(*decode);
+  *scores_off = *lse_off + up256((size_t)batch * hq * sizeof(float));
+  *total = *scores_off + (size_t)batch * hq * max_blocks * kPage * sizeof(float);
+  return ODA_OK;
+}
+
+static int decode_mass(const oda_kv* kv, const oda_kv4* kv4, const oda_visibility* vis, const void* q,
+                       int hq, float scale, const void* k_new, const void* v_new, void* out,
+                       int out_dtype, float* lse, const float* mass_in, float* mass_out,
+                       int64_t mass_tokens, void* ws, size_t ws_bytes, void* stream) {
+  if (vis == nullptr) return ODA_ERR_INVALID_ARG;
+  int rc = check_kv(kv);
+  if (rc != ODA_OK) return rc;
+  if ((rc = check_visibility(kv, vis)) != ODA_OK) return rc;
+  if ((rc = check_decode_args(kv, *vis, q, hq, scale, k_new, v_new, out, out_dtype, lse, ws)) != ODA_OK)
+    return rc;
+  const long long cap = (long long)kv->max_blocks_per_seq * kPage;
+  if (mass_tokens < cap || mass_tokens % 4 != 0) return ODA_ERR_INVALID_ARG;
+  if (cap >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
+  if (kv->batch == 0) return ODA_OK;
+  if (mass_out == nullptr || !aligned_or_null(mass_out, 16) || !aligned_or_null(mass_in, 16))
+    return ODA_ERR_INVALID_ARG;
+  size_t decode = 0, lse_off = 0, scores_off = 0, total = 0;
+  rc = mass_ws(kv->batch, kv->num_kv_heads, hq, kv->max_blocks_per_seq, kv4 != nullptr, &decode, &lse_off,
+               &scores_off, &total);
+  if (rc != ODA_OK) return rc;
+  if (ws_bytes < total) return ODA_ERR_WORKSPACE_TOO_SMALL;
+  const long long blocks_per_row = (cap + 4 * kMassThreads - 1) / (4 * kMassThreads);
+  if (blocks_per_row * kv->batch * kv->num_kv_heads >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  float* l = lse != nullptr ? lse : reinterpret_cast<float*>(w + lse_off);
+  float* scores = reinterpret_cast<float*>(w + scores_off);
+  rc = kv4 != nullptr ? launch_kv4_decode(kv4, vis, q, hq, scale, k_new, v_new, out, out_dtype, l, scores,
+                                          (int)cap, ws, decode, stream)
+                      : launch_decode_scores(kv, *vis, q, hq, scale, k_new, v_new, out, out_dtype, l,
+                                             scores, (int)cap, ws, decode, stream);
+  if (rc != ODA_OK) return rc;
+
+  MassParams p;
+  p.plan = plan_args(kv, *vis);
+  p.hkv = kv->num_kv_heads;
+  p.hq = hq;
+  p.group = hq / kv->num_kv_heads;
+  p.scores = scores;
+  p.cap = (int)cap;
+  p.lse = l;
+  p.mass_in = mass_in;
+  p.mass_out = mass_out;
+  p.mass_tokens = mass_tokens;
+  p.blocks_per_row = (int)blocks_per_row;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks_per_row * kv->batch * kv->num_kv_heads));
+  cfg.blockDim = dim3(kMassThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(mass_out == mass_in ? cudaLaunchKernelEx(&cfg, mass_kernel<true>, p)
+                                         : cudaLaunchKernelEx(&cfg, mass_kernel<false>, p));
+}
+
+}  // namespace oda
+
+using namespace oda;
+
+extern "C" int oda_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
+                                              int32_t max_blocks_per_seq, size_t* bytes) {
+  size_t d, l, s;
+  return bytes == nullptr ? ODA_ERR_INVALID_ARG
+                          : mass_ws(batch, num_kv_heads, num_q_heads, max_blocks_per_seq, false, &d, &l, &s,
+                                    bytes);
+}
+
+extern "C" int oda_kv4_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads,
+                                                  int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                                  size_t* bytes) {
+  size_t d, l, s;
+  return bytes == nullptr ? ODA_ERR_INVALID_ARG
+                          : mass_ws(batch, num_kv_heads, num_q_heads, max_blocks_per_seq, true, &d, &l, &s,
+                                    bytes);
+}
+
+extern "C" int oda_decode_mass(const oda_kv* kv, const oda_visibility* vis, const void* q,
+                               int32_t num_q_heads, float scale, const void* k_new, const void* v_new,
+                               void* out, int32_t out_dtype, float* lse, const float* mass_in,
+                               float* mass_out, int64_t mass_tokens, void* ws, size_t ws_bytes,
+                               void* stream) {
+  return decode_mass(kv, nullptr, vis, q, num_q_heads, scale, k_new, v_new, out, out_dtype, lse, mass_in,
+                     mass_out, mass_tokens, ws, ws_bytes, stream);
+}
+
+extern "C" int oda_kv4_decode_mass(const oda_kv4* kv, const oda_visibility* vis, const void* q,
+                                   int32_t num_q_heads, float scale, const void* k_new,
+                                   const void* v_new, void* out, int32_t out_dtype, float* lse,
+                                   const float* mass_in, float* mass_out, int64_t mass_tokens, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  const int rc = check_kv4(kv);
+  if (rc != ODA_OK) return rc;
+  const oda_kv k = kv4_as_kv(kv);
+  return decode_mass(&k, kv, vis, q, num_q_heads, scale, k_new, v_new, out, out_dtype, lse, mass_in,
+                     mass_out, mass_tokens, ws, ws_bytes, stream);
+}

@@ -63,6 +63,9 @@ struct PlanArgs {
   int pos_lo, pos_hi;          // Shard
 };
 
+// Host (oda_decode.cu): the plan arguments of a visibility rule applied to a cache.
+PlanArgs plan_args(const oda_kv* kv, const oda_visibility& v);
+
 // Append logical pages [first, last] to the run list; runs arrive in ascending order of
 // `first`, and a run that touches or overlaps the previous one extends it. Every index is a
 // compile-time constant, so the plan stays in registers.

@@ -38,6 +38,8 @@ ODA_DA_LOCAL = 2
 ODA_STAT_ROWS = 0
 ODA_STAT_PAGES = 1
 ODA_STATS_LEN = 2
+ODA_KV4_PAGE_BYTES = 2304
+ODA_KV4_GROUP = 64
 ODA_PHASE_LOCAL = 1
 ODA_PHASE_RECALL = 2
 ODA_PHASE_FULL = 4
@@ -65,6 +67,17 @@ class OdaError(RuntimeError):
 class oda_kv(ctypes.Structure):
     _fields_ = [
         ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("batch", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("max_blocks_per_seq", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+        ("dev_status", ctypes.c_void_p), ("stats", ctypes.c_void_p),
+    ]
+
+
+class oda_kv4(ctypes.Structure):
+    _fields_ = [
+        ("cache", ctypes.c_void_p),
         ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
         ("batch", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
         ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
@@ -115,6 +128,9 @@ _I = ctypes.c_int32
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
+_L = ctypes.c_int64
+
+_KV4 = ctypes.POINTER(oda_kv4)
 _VIS = ctypes.POINTER(oda_visibility)
 
 _SIGNATURES = {
@@ -138,6 +154,19 @@ _SIGNATURES = {
                                             _F, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "oda_recall_score": (ctypes.c_int, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _F, _F, _P, _P, _P,
                                         ctypes.c_ulonglong, _P, _SZ, _P]),
+    "oda_kv4_append": (ctypes.c_int, [_KV4, _P, _P, _L, _L, _I, _P, _P, _P]),
+    "oda_kv4_read": (ctypes.c_int, [_KV4, _P, _P, _I, _I, _P, _P]),
+    "oda_kv4_decode_workspace_size": (ctypes.c_int, [_I, _I, _I, ctypes.POINTER(_SZ)]),
+    "oda_kv4_decode": (ctypes.c_int, [_KV4, _VIS, _P, _I, _F, _P, _P, _P, _I, _P, _P, _SZ, _P]),
+    "oda_decode_mass_workspace_size": (ctypes.c_int, [_I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "oda_kv4_decode_mass_workspace_size": (ctypes.c_int, [_I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "oda_decode_mass": (ctypes.c_int, [_KV, _VIS, _P, _I, _F, _P, _P, _P, _I, _P, _P, _P, _L, _P, _SZ,
+                                       _P]),
+    "oda_kv4_decode_mass": (ctypes.c_int, [_KV4, _VIS, _P, _I, _F, _P, _P, _P, _I, _P, _P, _P, _L, _P,
+                                           _SZ, _P]),
+    "oda_kv_evict_workspace_size": (ctypes.c_int, [_I, ctypes.POINTER(_SZ)]),
+    "oda_kv_evict": (ctypes.c_int, [_KV, _P, _L, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _SZ, _P]),
+    "oda_kv4_evict": (ctypes.c_int, [_KV4, _P, _L, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _SZ, _P]),
     "oda_step_graph_create": (ctypes.c_int, [ctypes.POINTER(oda_step_desc), _P,
                                              ctypes.POINTER(ctypes.c_void_p)]),
     "oda_step_graph_launch": (ctypes.c_int, [_P, _P]),
@@ -366,6 +395,210 @@ def oda_recall_score(h_prev, emb, h_local, w1, b1, w2, b2: float, theta: float, 
         _ptr(gate_out, torch.int32, "gate_out"), _ptr(full_count, torch.int64, "full_count"),
         int(graph_cond_handle), _ptr(ws, None, "ws"), ws.numel() * ws.element_size(),
         _stream(stream)), "oda_recall_score")
+
+
+# ---- 4-bit cache, decode with accumulated weights, eviction ------------------------------------
+def make_kv4(cache, block_table, seq_lens, dev_status=None, stats=None) -> oda_kv4:
+    """oda_kv4 for a uint8 cache [num_blocks][Hkv][ODA_KV4_PAGE_BYTES], int32 block_table [B][maxb] and
+    int32 seq_lens [B] (tokens including the current one)."""
+    nb, hkv, nbytes = cache.shape
+    if nbytes != ODA_KV4_PAGE_BYTES:
+        raise ValueError("cache pages must be %d bytes, got %d" % (ODA_KV4_PAGE_BYTES, nbytes))
+    kv = oda_kv4(
+        cache=_ptr(cache, torch.uint8, "cache"),
+        block_table=_ptr(block_table, torch.int32, "block_table"),
+        seq_lens=_ptr(seq_lens, torch.int32, "seq_lens"),
+        batch=block_table.shape[0], num_kv_heads=hkv, head_dim=128, block_size=16,
+        max_blocks_per_seq=block_table.shape[1], num_blocks=nb,
+        dev_status=_ptr(dev_status, torch.int32, "dev_status"),
+        stats=_ptr(stats, torch.int64, "stats"))
+    kv._refs = (cache, block_table, seq_lens, dev_status, stats)
+    return kv
+
+
+def _kv_device(kv) -> Optional[int]:
+    """The device of a cache made by make_kv / make_kv4 (None for a handle made by hand)."""
+    refs = getattr(kv, "_refs", None)
+    return refs[0].device.index if refs else None
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _call(kv, name, stream, args, tensors):
+    """Call an entry point on the cache's device. Every tensor lives there; without a stream
+    argument the work goes to that device's current stream."""
+    dev = _kv_device(kv)
+    for t in tensors:
+        if t is not None and dev is not None and t.device.index != dev:
+            raise ValueError("%s: every tensor must be on the cache's device cuda:%d, got %s"
+                             % (name, dev, t.device))
+    fn = getattr(load(), name)
+    if dev is None or dev == torch.cuda.current_device():
+        _check(fn(ctypes.byref(kv), *args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(ctypes.byref(kv), *args, _stream(stream)), name)
+
+
+def _row_stride(t, hkv: int, name) -> int:
+    """Element stride of rows [n][hkv][128] whose heads and dims are dense."""
+    if t.dim() != 3 or t.shape[1] != hkv or t.shape[2] != 128:
+        raise ValueError("%s must have shape (rows, %d, 128), got %s" % (name, hkv, tuple(t.shape)))
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError("%s must be a CUDA bfloat16 tensor" % name)
+    if t.stride(2) != 1 or (hkv > 1 and t.stride(1) != 128):
+        raise ValueError("%s: heads and dims must be dense" % name)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), hkv * 128)
+
+
+def _check_cu_rows(kv, cu_rows, num_rows):
+    if cu_rows is None:
+        if num_rows != kv.batch:
+            raise ValueError("without cu_rows there is one row per sequence: %d rows, batch %d"
+                             % (num_rows, kv.batch))
+    else:
+        _shape(cu_rows, (kv.batch + 1,), "cu_rows")
+
+
+def oda_kv4_append(kv: oda_kv4, k_new, v_new, cu_rows=None, gate=None, stream=None):
+    """Quantise bf16 rows [n][Hkv][128] (rows may be strided) into the last slots of their sequences:
+    one row per sequence, or rows cu_rows[b] .. cu_rows[b + 1] - 1 (int32 [B + 1]) to sequence b."""
+    ks, vs = _row_stride(k_new, kv.num_kv_heads, "k_new"), _row_stride(v_new, kv.num_kv_heads, "v_new")
+    _shape(v_new, k_new.shape, "v_new")
+    _check_cu_rows(kv, cu_rows, k_new.shape[0])
+    if gate is not None:
+        _shape(gate, (kv.batch,), "gate")
+    _call(kv, "oda_kv4_append", stream,
+          (k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_new.shape[0],
+           _ptr(cu_rows, torch.int32, "cu_rows"), _ptr(gate, torch.int32, "gate")),
+          (k_new, v_new, cu_rows, gate))
+
+
+def oda_kv4_read(kv: oda_kv4, k_out, v_out, cu_rows=None, stream=None):
+    """Values of the slots oda_kv4_append would write, into k_out, v_out [n][Hkv][128] (fp32 or bf16)."""
+    _shape(k_out, (k_out.shape[0], kv.num_kv_heads, 128), "k_out")
+    _shape(v_out, k_out.shape, "v_out")
+    if v_out.dtype != k_out.dtype:
+        raise ValueError("k_out and v_out must have one dtype")
+    _check_cu_rows(kv, cu_rows, k_out.shape[0])
+    _call(kv, "oda_kv4_read", stream,
+          (_ptr(k_out, None, "k_out"), _ptr(v_out, None, "v_out"), _out_dtype(k_out), k_out.shape[0],
+           _ptr(cu_rows, torch.int32, "cu_rows")), (k_out, v_out, cu_rows))
+
+
+def _check_decode(kv, q, out, k_new, v_new, lse):
+    hq = q.shape[1]
+    _shape(q, (kv.batch, hq, 128), "q")
+    _shape(out, (kv.batch, hq, 128), "out")
+    if k_new is not None:
+        _shape(k_new, (kv.batch, kv.num_kv_heads, 128), "k_new")
+    if v_new is not None:
+        _shape(v_new, (kv.batch, kv.num_kv_heads, 128), "v_new")
+    if lse is not None:
+        _shape(lse, (kv.batch, hq), "lse")
+    return hq
+
+
+def oda_kv4_decode(kv: oda_kv4, vis: oda_visibility, q, scale: float, out, ws, k_new=None,
+                   v_new=None, lse=None, stream=None):
+    """Decode attention over the 4-bit cache under any visibility rule (oda_visibility)."""
+    hq = _check_decode(kv, q, out, k_new, v_new, lse)
+    _call(kv, "oda_kv4_decode", stream,
+          (ctypes.byref(vis), _ptr(q, torch.bfloat16, "q"), hq, scale,
+           _ptr(k_new, torch.bfloat16, "k_new"), _ptr(v_new, torch.bfloat16, "v_new"),
+           _ptr(out, None, "out"), _out_dtype(out), _ptr(lse, torch.float32, "lse"),
+           _ptr(ws, None, "ws"), ws.numel() * ws.element_size()), (q, out, ws, k_new, v_new, lse))
+
+
+def _size(name, *args) -> int:
+    n = _SZ(0)
+    _check(getattr(load(), name)(*args, ctypes.byref(n)), name)
+    return n.value
+
+
+def oda_kv4_decode_workspace_size(batch: int, num_kv_heads: int, num_q_heads: int) -> int:
+    return _size("oda_kv4_decode_workspace_size", batch, num_kv_heads, num_q_heads)
+
+
+def oda_decode_mass_workspace_size(batch: int, num_kv_heads: int, num_q_heads: int,
+                                   max_blocks_per_seq: int) -> int:
+    return _size("oda_decode_mass_workspace_size", batch, num_kv_heads, num_q_heads, max_blocks_per_seq)
+
+
+def oda_kv4_decode_mass_workspace_size(batch: int, num_kv_heads: int, num_q_heads: int,
+                                       max_blocks_per_seq: int) -> int:
+    return _size("oda_kv4_decode_mass_workspace_size", batch, num_kv_heads, num_q_heads,
+                 max_blocks_per_seq)
+
+
+def oda_kv_evict_workspace_size(batch: int) -> int:
+    return _size("oda_kv_evict_workspace_size", batch)
+
+
+def _decode_mass(name, kv, vis, q, scale, out, ws, mass_out, mass_in, k_new, v_new, lse, stream):
+    hq = _check_decode(kv, q, out, k_new, v_new, lse)
+    _shape(mass_out, (kv.batch, kv.num_kv_heads, mass_out.shape[2]), "mass_out")
+    if mass_in is not None:
+        _shape(mass_in, mass_out.shape, "mass_in")
+    _call(kv, name, stream,
+          (ctypes.byref(vis), _ptr(q, torch.bfloat16, "q"), hq, scale,
+           _ptr(k_new, torch.bfloat16, "k_new"), _ptr(v_new, torch.bfloat16, "v_new"),
+           _ptr(out, None, "out"), _out_dtype(out), _ptr(lse, torch.float32, "lse"),
+           _ptr(mass_in, torch.float32, "mass_in"), _ptr(mass_out, torch.float32, "mass_out"),
+           mass_out.shape[2], _ptr(ws, None, "ws"), ws.numel() * ws.element_size()),
+          (q, out, ws, k_new, v_new, lse, mass_in, mass_out))
+
+
+def oda_decode_mass(kv: oda_kv, vis: oda_visibility, q, scale: float, out, ws, mass_out, mass_in=None,
+                    k_new=None, v_new=None, lse=None, stream=None):
+    """oda_decode, and mass_out = mass_in + the softmax weight of every position, summed over the query
+    heads of each KV head (fp32 [B][Hkv][tokens]). mass_in may be mass_out; None counts as zero."""
+    _decode_mass("oda_decode_mass", kv, vis, q, scale, out, ws, mass_out, mass_in, k_new, v_new, lse,
+                 stream)
+
+
+def oda_kv4_decode_mass(kv: oda_kv4, vis: oda_visibility, q, scale: float, out, ws, mass_out,
+                        mass_in=None, k_new=None, v_new=None, lse=None, stream=None):
+    """oda_kv4_decode, and mass_out = mass_in + attention weights as in oda_decode_mass."""
+    _decode_mass("oda_kv4_decode_mass", kv, vis, q, scale, out, ws, mass_out, mass_in, k_new, v_new, lse,
+                 stream)
+
+
+def _evict(name, kv, mass, sink, recent, budget, dst_block_table, kept, mass_out, seq_lens_out, ws, gate,
+           stream):
+    _shape(mass, (kv.batch, kv.num_kv_heads, mass.shape[2]), "mass")
+    _shape(mass_out, mass.shape, "mass_out")
+    _shape(kept, (kv.batch, kv.num_kv_heads, budget), "kept")
+    _shape(dst_block_table, (kv.batch, dst_block_table.shape[1]), "dst_block_table")
+    _shape(seq_lens_out, (kv.batch,), "seq_lens_out")
+    if gate is not None:
+        _shape(gate, (kv.batch,), "gate")
+    _call(kv, name, stream,
+          (_ptr(mass, torch.float32, "mass"), mass.shape[2], sink, recent, budget,
+           _ptr(gate, torch.int32, "gate"), _ptr(dst_block_table, torch.int32, "dst_block_table"),
+           dst_block_table.shape[1], _ptr(kept, torch.int32, "kept"),
+           _ptr(mass_out, torch.float32, "mass_out"), _ptr(seq_lens_out, torch.int32, "seq_lens_out"),
+           _ptr(ws, None, "ws"), ws.numel() * ws.element_size()),
+          (mass, gate, dst_block_table, kept, mass_out, seq_lens_out, ws))
+
+
+def oda_kv_evict(kv: oda_kv, mass, sink: int, recent: int, budget: int, dst_block_table, kept, mass_out,
+                 seq_lens_out, ws, gate=None, stream=None):
+    """Cut every sequence down to `budget` slots per KV head: the first `sink`, the last `recent` and the
+    heaviest others by mass (fp32 [B][Hkv][tokens]), moved in order to the pages of dst_block_table. In
+    place: dst_block_table, mass_out and seq_lens_out may be the cache's own block_table, mass, seq_lens."""
+    _evict("oda_kv_evict", kv, mass, sink, recent, budget, dst_block_table, kept, mass_out, seq_lens_out,
+           ws, gate, stream)
+
+
+def oda_kv4_evict(kv: oda_kv4, mass, sink: int, recent: int, budget: int, dst_block_table, kept, mass_out,
+                  seq_lens_out, ws, gate=None, stream=None):
+    """oda_kv_evict over a 4-bit cache."""
+    _evict("oda_kv4_evict", kv, mass, sink, recent, budget, dst_block_table, kept, mass_out, seq_lens_out,
+           ws, gate, stream)
 
 
 def _ptr_array(tensors: Sequence, dtype, name):
