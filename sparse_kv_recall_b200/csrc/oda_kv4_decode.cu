@@ -32,7 +32,8 @@ namespace oda {
 
 constexpr int kW4 = 8;               // warps per CTA
 constexpr int kThreads4 = kW4 * 32;
-constexpr int kSlots4 = 5;           // pages in flight per warp
+constexpr int kSlots4 = 4;           // pages a warp holds in shared memory
+constexpr int kRefs4 = 64;           // page references a warp holds (two halves, refilled in turn)
 constexpr int kCtasPerSm4 = 2;
 constexpr int kMinShare4 = 8;        // units per CTA at least (one page per warp)
 constexpr int kPStride = 48;         // words per (page, head) of the weight exchange
@@ -137,7 +138,8 @@ struct Kv4State {
   float acc[8][4];     // tile 4 g + j: dims 64 g + 8 gid + j (0, 1) and + j + 4 (2, 3); columns
 };                     // 2 tig, 2 tig + 1 are the two parts of head tig
 
-constexpr float kR0 = 1.2676506e30f;  // 2^100
+constexpr float kR0 = 1.2676506e30f;   // 2^100
+constexpr float kNoMax = -1e30f;       // running maximum before any visible score
 
 // The group's q as B fragments and per-column sums. Returns the power of two that undoes q's.
 template <int G>
@@ -179,10 +181,11 @@ __device__ __forceinline__ float load_q4(const __nv_bfloat16* q, int lane, uint3
   return __uint_as_float((254u - f) << 23);
 }
 
-struct PageView {
-  const unsigned char* st;  // the page in shared memory (any page's, if this one is not there)
-  int pos;                  // its first position
-  bool ok;                  // it was read
+// A page of a warp's share: where it lies and which of its rows count.
+struct PageEntry {
+  int pos;   // first position + visible rows - 1 (a page's first position is a multiple of 16);
+             // negative: nothing to read (past the share's end, or reported)
+  int page;  // physical page
 };
 
 // Visible rows among the 16 positions from `pos`.
@@ -192,10 +195,11 @@ __device__ __forceinline__ int rows_in_page(const SeqPlan& s, int pos) {
   return max(0, hi - lo + 1) - max(0, ghi - glo + 1);
 }
 
-// One step: kPages pages. kq undoes q's power of two and carries the softmax scale in base 2;
-// qs is sum q times that scale.
+// One step over the kPages pages at `stage` (a page that is not there holds stale bytes: its codes
+// are finite numbers whatever they are, its scales and minima are not used). entry[n] as above. kq
+// undoes q's power of two and carries the softmax scale in base 2; qs is sum q times that scale.
 template <int G, bool kScores>
-__device__ __forceinline__ void kv4_step(const PageView (&pg)[Roles<G>::kPages], bool all_visible,
+__device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (&entry)[Roles<G>::kPages],
                                          const SeqPlan& sp, const uint32_t (&qb)[8][2], float kq,
                                          const float (&qs)[2], Kv4State& st, uint32_t* pw,
                                          float* scores, int cap, int lane) {
@@ -206,10 +210,11 @@ __device__ __forceinline__ void kv4_step(const PageView (&pg)[Roles<G>::kPages],
 
   // ---- scores: c[page][token gid: 0, 1; gid + 8: 2, 3][columns 2 tig, 2 tig + 1] ----
   float c[NP][4];
+  const unsigned char* kbase = stage + gid * kKv4RowBytes + 16 * tig;
 #pragma unroll
   for (int n = 0; n < NP; ++n) {
-    const uint4 wa = *reinterpret_cast<const uint4*>(pg[n].st + gid * kKv4RowBytes + 16 * tig);
-    const uint4 wb = *reinterpret_cast<const uint4*>(pg[n].st + (gid + 8) * kKv4RowBytes + 16 * tig);
+    const uint4 wa = *reinterpret_cast<const uint4*>(kbase + n * kKv4PageBytes);
+    const uint4 wb = *reinterpret_cast<const uint4*>(kbase + n * kKv4PageBytes + 8 * kKv4RowBytes);
     const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
@@ -222,9 +227,9 @@ __device__ __forceinline__ void kv4_step(const PageView (&pg)[Roles<G>::kPages],
       mma_16816_f16(c[n], ca[2], cb[2], ca[3], cb[3], qb[2 * e + 1][0], qb[2 * e + 1][1]);
     }
   }
-  const PageView& my = (NP == 2 && mypage) ? pg[NP - 1] : pg[0];
-  const uint4 ma = *reinterpret_cast<const uint4*>(my.st + kKv4MetaOff + gid * kKv4MetaBytes);
-  const uint4 mb = *reinterpret_cast<const uint4*>(my.st + kKv4MetaOff + (gid + 8) * kKv4MetaBytes);
+  const unsigned char* mbase = stage + mypage * kKv4PageBytes + kKv4MetaOff + gid * kKv4MetaBytes;
+  uint4 ma = *reinterpret_cast<const uint4*>(mbase);
+  uint4 mb = *reinterpret_cast<const uint4*>(mbase + 8 * kKv4MetaBytes);
   float cc[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) cc[i] = (NP == 2 && mypage) ? c[NP - 1][i] : c[0][i];
@@ -237,20 +242,30 @@ __device__ __forceinline__ void kv4_step(const PageView (&pg)[Roles<G>::kPages],
   float x0 = (mygrp ? s01 : s00) + __shfl_xor_sync(0xffffffffu, mygrp ? s00 : s01, R::kOther);
   float x1 = (mygrp ? s11 : s10) + __shfl_xor_sync(0xffffffffu, mygrp ? s10 : s11, R::kOther);
 
+  const int mine = (NP == 2 && mypage) ? entry[NP - 1] : entry[0];
   bool v0 = true, v1 = true;
-  if (!all_visible) {
-    v0 = my.ok && row_visible(sp, my.pos + gid);
-    v1 = my.ok && row_visible(sp, my.pos + gid + 8);
+  const bool part = NP == 2 ? ((entry[0] & entry[NP - 1]) & 15) != 15 || (entry[0] | entry[NP - 1]) < 0
+                            : (entry[0] & 15) != 15 || entry[0] < 0;
+  if (part) {  // (uniform) some row of these pages is hidden or absent: nothing of it may count
+    const int pos = mine & ~15;
+    v0 = mine >= 0 && row_visible(sp, pos + gid);
+    v1 = mine >= 0 && row_visible(sp, pos + gid + 8);
+    if (!v0) {
+      x0 = -INFINITY;
+      ma.z = ma.w = 0u;
+    }
+    if (!v1) {
+      x1 = -INFINITY;
+      mb.z = mb.w = 0u;
+    }
   }
   if constexpr (kScores) {
     if (myhead < G) {
-      float* dst = scores + (size_t)myhead * cap + my.pos;
+      float* dst = scores + (size_t)myhead * cap + (mine & ~15);
       if (v0) dst[gid] = x0;
       if (v1) dst[gid + 8] = x1;
     }
   }
-  x0 = v0 ? x0 : -INFINITY;
-  x1 = v1 ? x1 : -INFINITY;
 
   // ---- online softmax; the maximum is raised only when a score passes it by 2^kLazyMax ----
   if (__any_sync(0xffffffffu, fmaxf(x0, x1) > st.m + kLazyMax)) {
@@ -260,7 +275,7 @@ __device__ __forceinline__ void kv4_step(const PageView (&pg)[Roles<G>::kPages],
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
     const bool up = mx > st.m + kLazyMax;
-    const float al = !up ? 1.f : (st.m == -INFINITY ? 0.f : ex2_fast(st.m - mx));
+    const float al = up ? ex2_fast(st.m - mx) : 1.f;
     if (up) st.m = mx;
     st.l *= al;
     st.corr[0] *= al;
@@ -271,12 +286,11 @@ __device__ __forceinline__ void kv4_step(const PageView (&pg)[Roles<G>::kPages],
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.acc[t][i] *= ah;
   }
-  const float p0 = x0 == -INFINITY ? 0.f : ex2_fast(x0 - st.m);
-  const float p1 = x1 == -INFINITY ? 0.f : ex2_fast(x1 - st.m);
+  const float p0 = ex2_fast(x0 - st.m), p1 = ex2_fast(x1 - st.m);
   st.l += p0 + p1;
 
   // ---- weights times the V scales, as two fp16 each ----
-  const uint32_t va[2] = {v0 ? ma.z : 0u, v0 ? ma.w : 0u}, vb[2] = {v1 ? mb.z : 0u, v1 ? mb.w : 0u};
+  const uint32_t va[2] = {ma.z, ma.w}, vb[2] = {mb.z, mb.w};
   float y0[2], y1[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
@@ -323,13 +337,13 @@ __device__ __forceinline__ void kv4_step(const PageView (&pg)[Roles<G>::kPages],
   __syncwarp();
 
   // ---- P.V ----
-  const int bh = (gid >> 1) & (HG - 1), part = gid & 1;
+  const int bh = (gid >> 1) & (HG - 1), col = gid & 1;
 #pragma unroll
   for (int n = 0; n < NP; ++n) {
-    const uint32_t* src = pw + (n * HG + bh) * kPStride + 2 * part;
+    const uint32_t* src = pw + (n * HG + bh) * kPStride + 2 * col;
     const uint2 b0 = *reinterpret_cast<const uint2*>(src + 4 * tig);
     const uint2 b1 = *reinterpret_cast<const uint2*>(src + 4 * (tig + 4));
-    const unsigned char* vs = pg[n].st + kKv4VOff + tig * kKv4RowBytes + 8 * gid;
+    const unsigned char* vs = stage + n * kKv4PageBytes + kKv4VOff + tig * kKv4RowBytes + 8 * gid;
     const uint2 w0 = *reinterpret_cast<const uint2*>(vs);
     const uint2 w1 = *reinterpret_cast<const uint2*>(vs + 8 * kKv4RowBytes);
     const uint2 w2 = *reinterpret_cast<const uint2*>(vs + 4 * kKv4RowBytes);
@@ -365,7 +379,8 @@ struct Kv4Smem {
   static constexpr int kSlotsOff = 0;
   static constexpr int kBarsOff = kW4 * kSlots4 * kKv4PageBytes;
   static constexpr int kPOff = kBarsOff + (kW4 * kSlots4 * 8 + 15) / 16 * 16;
-  static constexpr int kPreOff = kPOff + kW4 * kPWords * 4;
+  static constexpr int kRefOff = kPOff + kW4 * kPWords * 4;
+  static constexpr int kPreOff = kRefOff + kW4 * kRefs4 * (int)sizeof(PageEntry);
   static constexpr int kBytes = kPreOff + (kMaxBatch + 1) * 4;
 };
 
@@ -379,7 +394,9 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   unsigned char* slots = smem + Kv4Smem::kSlotsOff + warp * kSlots4 * kKv4PageBytes;
+  constexpr int kStages = kSlots4 / NP;  // of NP pages, one barrier each
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Kv4Smem::kBarsOff) + warp * kSlots4;
+  PageEntry* refs = reinterpret_cast<PageEntry*>(smem + Kv4Smem::kRefOff) + warp * kRefs4;
   uint32_t* pw = reinterpret_cast<uint32_t*>(smem + Kv4Smem::kPOff) + warp * kPWords;
   int* pre = reinterpret_cast<int*>(smem + Kv4Smem::kPreOff);
   const int B = p.batch, Hkv = p.hkv;
@@ -387,7 +404,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
 
   // ---- prefix of visible units per sequence, share alignment ----
   if (lane == 0) {
-    for (int s = 0; s < kSlots4; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], NP);
     fence_barrier_init();
   }
   if (tid == 0) {
@@ -435,7 +452,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     else if (Pe >= s_align) Pe -= Pe % s_align;
   }
   const uint64_t policy = l2_evict_first_policy();
-  unsigned wcount = 0;
+  unsigned wcount = 0;  // stages this warp has used
   bool dead = false;
   long long x = cta < Pe ? (T * cta) / Pe : 0;
   const long long x_end = cta < Pe ? (T * (cta + 1)) / Pe : 0;
@@ -459,33 +476,49 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     // this warp's pages: runs of NP consecutive list entries, strided over the warps
     const int steps = (j1 - j0 + NP - 1) / NP;
     const int my_steps = steps > warp ? (steps - warp + kW4 - 1) / kW4 : 0;
-    const int cnt = my_steps * NP;  // page n of this warp: entry j0 + (n / NP * kW4 + warp) * NP + n % NP
-    auto entry = [&](int n) { return j0 + ((n / NP) * kW4 + warp) * NP + n % NP; };
-    auto ref_of = [&](int n) {
-      PageRef r;
-      r.lp = 0;
-      r.pb = 0;
-      r.err = -1;  // past the share's end
-      const int j = n < cnt ? entry(n) : j1;
-      return j < j1 ? page_ref(p.plan, sp, b, j) : r;
+    // page n of this warp is list entry j0 + (n / NP * kW4 + warp) * NP + n % NP
+    unsigned rows_vis = 0, pages_read = 0;  // this lane's pages
+    auto fill = [&](int n0) {  // references of pages n0 .. n0 + 31
+      const int n = n0 + lane;
+      const int j = j0 + ((n / NP) * kW4 + warp) * NP + n % NP;
+      PageEntry e;
+      e.pos = -1;
+      e.page = 0;
+      if (n < my_steps * NP && j < j1) {
+        const PageRef r = page_ref(p.plan, sp, b, j);
+        if (r.err != 0) {
+          report(p.status, r.err);
+        } else {
+          const int rows = rows_in_page(sp, r.lp * kPage);
+          if (rows > 0) e.pos = r.lp * kPage + rows - 1;
+          e.page = r.pb;
+          rows_vis += rows;
+          ++pages_read;
+        }
+      }
+      refs[n % kRefs4] = e;
     };
-    auto issue = [&](int n) {  // lane 0: bring page n into its slot
-      const PageRef r = ref_of(n);
-      const unsigned k = wcount + n;
-      uint64_t* bar = &bars[k % kSlots4];
+    auto issue = [&](int step) {  // lanes below NP: bring a step's pages into its stage
+      const PageEntry e = refs[(step * NP + lane) % kRefs4];
+      const unsigned k = wcount + step;
+      uint64_t* bar = &bars[k % kStages];
       if (p.test_stall == 1 && cta == 0 && warp == 0 && k == 0) {
         mbar_arrive_expect_tx(bar, 16u);  // test hook: bytes that never arrive
-      } else if (r.err == 0) {
+      } else if (e.pos >= 0) {
         mbar_arrive_expect_tx(bar, kKv4PageBytes);
-        bulk_load(slots + (k % kSlots4) * kKv4PageBytes,
-                  p.cache + ((size_t)r.pb * Hkv + g) * kKv4PageBytes, kKv4PageBytes, bar, policy);
+        bulk_load(slots + ((k % kStages) * NP + lane) * kKv4PageBytes,
+                  p.cache + ((size_t)e.page * Hkv + g) * kKv4PageBytes, kKv4PageBytes, bar, policy);
       } else {
-        if (r.err > 0) report(p.status, r.err);
         mbar_arrive(bar);
       }
     };
-    if (!dead && lane == 0)
-      for (int n = 0; n < min(cnt, kSlots4); ++n) issue(n);
+    if (!dead) {
+      fill(0);
+      if (my_steps * NP > 32) fill(32);
+      __syncwarp();
+      if (lane < NP)
+        for (int s = 0; s < min(my_steps, kStages); ++s) issue(s);
+    }
     __syncwarp();
 
     uint32_t qb[8][2];
@@ -497,7 +530,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     if constexpr (kScores) scores = p.scores + ((size_t)b * p.hq + g * G) * p.cap;
 
     Kv4State st;
-    st.m = -INFINITY;
+    st.m = kNoMax;
     st.l = 0.f;
     st.corr[0] = st.corr[1] = 0.f;
     st.r[0] = st.r[1] = kR0;
@@ -505,54 +538,46 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     for (int t = 0; t < 8; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.acc[t][i] = 0.f;
-    unsigned rows_vis = 0, pages_read = 0;
 
-    for (int n = 0; n < cnt && !dead; n += NP) {
-      PageView pg[NP];
-      bool all_visible = true;
+    for (int s = 0; s < my_steps && !dead; ++s) {
+      if (s > 0 && s % (32 / NP) == 0 && s * NP + 32 < my_steps * NP) {
+        fill(s * NP + 32);  // the half that was used up last
+        __syncwarp();
+      }
+      const unsigned k = wcount + s;
+      unsigned char* stage = slots + (k % kStages) * NP * kKv4PageBytes;
+      int entry[NP];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const unsigned k = wcount + n + i;
-        const PageRef r = ref_of(n + i);
-        unsigned char* slot = slots + (k % kSlots4) * kKv4PageBytes;
-        if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bars[k % kSlots4], (k / kSlots4) & 1u, p.wait_ns))) {
-          if (lane == 0) report(p.status, ODA_DEV_TIMEOUT);
-          // let the copies already started into the other slots land, then stop
-          for (int m = n + i + 1; m < min(cnt, n + kSlots4); ++m)
-            mbar_wait(&bars[(wcount + m) % kSlots4], ((wcount + m) / kSlots4) & 1u, p.wait_ns);
-          dead = true;
-        }
-        pg[i].st = slot;
-        pg[i].pos = r.lp * kPage;
-        pg[i].ok = r.err == 0;
-        if (pg[i].ok && !dead) {
-          if (p.k_new != nullptr && r.lp == sp.t / kPage) {
-            // commit: the step's K/V, quantised, take slot t in the cache and in this copy
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                (lane < 16 ? p.k_new : p.v_new) + (size_t)bg * kHeadDim + 8 * (lane & 15));
-            uint32_t meta;
-            const uint32_t word = kv4_quantise(v, lane, meta);
-            kv4_store_row(slot, sp.t % kPage, word, meta, lane);
-            kv4_store_row(p.cache + ((size_t)r.pb * Hkv + g) * kKv4PageBytes, sp.t % kPage, word, meta, lane);
-            fence_proxy_async_smem();  // this slot is refilled by a bulk copy later
-            __syncwarp();
-          }
-          const int rows = rows_in_page(sp, pg[i].pos);
-          rows_vis += rows;
-          ++pages_read;
-          all_visible &= rows == kPage;
-        } else {
-          all_visible = false;
+      for (int i = 0; i < NP; ++i) entry[i] = refs[(s * NP + i) % kRefs4].pos;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[k % kStages], (k / kStages) & 1u, p.wait_ns))) {
+        if (lane == 0) report(p.status, ODA_DEV_TIMEOUT);
+        // let the copies already started into the other stages land, then stop
+        for (int m = s + 1; m < min(my_steps, s + kStages); ++m)
+          mbar_wait(&bars[(wcount + m) % kStages], ((wcount + m) / kStages) & 1u, p.wait_ns);
+        dead = true;
+        break;
+      }
+      if (p.k_new != nullptr) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if (entry[i] < 0 || entry[i] / kPage != sp.t / kPage) continue;
+          // commit: the step's K/V, quantised, take slot t in the cache and in this copy
+          const uint4 v = *reinterpret_cast<const uint4*>((lane < 16 ? p.k_new : p.v_new) +
+                                                          (size_t)bg * kHeadDim + 8 * (lane & 15));
+          uint32_t meta;
+          const uint32_t word = kv4_quantise(v, lane, meta);
+          const int pb = refs[(s * NP + i) % kRefs4].page;
+          kv4_store_row(stage + i * kKv4PageBytes, sp.t % kPage, word, meta, lane);
+          kv4_store_row(p.cache + ((size_t)pb * Hkv + g) * kKv4PageBytes, sp.t % kPage, word, meta, lane);
+          fence_proxy_async_smem();  // this slot is refilled by a bulk copy later
+          __syncwarp();
         }
       }
-      if (dead) break;
-      kv4_step<G, kScores>(pg, all_visible, sp, qb, kq, qs, st, pw, scores, p.cap, lane);
-      if (lane == 0)
-        for (int i = 0; i < NP; ++i)
-          if (n + i + kSlots4 < cnt) issue(n + i + kSlots4);
+      kv4_step<G, kScores>(stage, entry, sp, qb, kq, qs, st, pw, scores, p.cap, lane);
+      if (lane < NP && s + kStages < my_steps) issue(s + kStages);
       __syncwarp();
     }
-    wcount += cnt;
+    wcount += my_steps;
 
     // ---- merge the CTA's warps ----
 #pragma unroll
@@ -566,9 +591,13 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
       st.corr[0] += __shfl_xor_sync(0xffffffffu, st.corr[0], 2);
       st.corr[1] += __shfl_xor_sync(0xffffffffu, st.corr[1], 2);
     }
-    if (p.stats != nullptr && lane == 0 && (rows_vis | pages_read)) {
-      atomicAdd(&s_rows, (unsigned long long)rows_vis);
-      atomicAdd(&s_pages, (unsigned long long)pages_read);
+    if (p.stats != nullptr) {
+      rows_vis = __reduce_add_sync(0xffffffffu, rows_vis);
+      pages_read = __reduce_add_sync(0xffffffffu, pages_read);
+      if (lane == 0 && (rows_vis | pages_read)) {
+        atomicAdd(&s_rows, (unsigned long long)rows_vis);
+        atomicAdd(&s_pages, (unsigned long long)pages_read);
+      }
     }
     __syncthreads();  // every warp is done with its slots: reuse them as merge scratch
     if (p.stats != nullptr && tid == 0) {
@@ -581,7 +610,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     float* Lw = Mw + kW4 * HG;                   // [kW4][HG]
     float* Aw = Lw + kW4 * HG;                   // [kW4][HG][128]
     if (gid == 0 && (NP == 1 || tig < 2)) {
-      Mw[warp * HG + R::head(tig)] = st.m;
+      Mw[warp * HG + R::head(tig)] = st.m == kNoMax ? -INFINITY : st.m;
       Lw[warp * HG + R::head(tig)] = st.l;
     }
     {
