@@ -8,20 +8,20 @@
 // pipe (half rate), which unpacks the codes. So both products run on the tensor cores straight from
 // codes, and scales and minima are applied to sums instead of to elements:
 //
-//   K:  s_p = sum_groups [ S_g sum_d (c - 8) q_d + (M_g + 8 S_g) sum_d q_d ]  (S, M of token p)
-//       mma.sync m16n8k16 fp16, A = 16 tokens x codes, B = columns (group, head) that hold q in the
-//       dims of their group and zero elsewhere, so one accumulator pair serves both groups.
-//   V:  o_d = sum_p (w_p S_g) (c - 7.5) + sum_p w_p (M_g + 7.5 S_g)
+//   K:  s_p = sum_groups [ S_g sum_d (c - 8) q_d + (M_g + 8 S_g) sum_d q_d ]   (S, M of token p)
+//       mma.sync m16n8k16 fp16, A = 16 tokens x codes, B = columns (head, group) that hold the head's q
+//       in the dims of their group and zero elsewhere. q is scaled by a power of two to the top of the
+//       fp16 range: its eight significant bits fit, so every dim within 2^-28 of the head's largest is
+//       exact.
+//   V:  o_d = sum_p (w_p S_g) (c - z_p) + sum_p w_p (M_g + z_p S_g)
 //       A = codes as dims x 16 tokens, B = w_p S_g as a sum of two fp16 (columns (head, part): 22
-//       bits); the second sum has one term per token and group and runs on the CUDA cores.
+//       bits); the second sum has one term per token and group and runs on the CUDA cores. The codes
+//       are centred, z_p = 8 and 7 in turn (7.5 on average): over a long history an offset would grow
+//       with the token count and the signal only with its square root. w S enters by a running power
+//       of two per head and group that is raised when a weight passes 2^15.
 //
-// A code becomes an fp16 by one and-or that puts its nibble into the mantissa of 1024 (K) or 512
-// (V, one bit further up: 512 + c has room for the half) and one fp16 fma that subtracts the
-// offset; both are exact. Codes are centred so that the sums hold no offset to cancel: over a long
-// history the offset would grow with the token count, the signal only with its square root.
-// q is scaled by a power of two to the top of the fp16 range (bf16 has 8 significant bits, so every
-// dim within 2^-28 of the largest is exact), w S by a running power of two per head and group
-// that is raised when a weight passes 2^15.
+// A code becomes an fp16 by an and-or that puts its nibble into the mantissa of 1024 and one exact
+// fp16 add or fma that takes the offset off.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -94,91 +94,85 @@ __device__ __forceinline__ float2 h2_unpack(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// Nibbles j of the two halves of w, as fp16 c - 8: j even in bits 0-3, odd in bits 4-7 of each
-// half of w (j < 2) or of w >> 8.
-__device__ __forceinline__ void k_codes(uint32_t w, uint32_t (&a)[4]) {
-  constexpr uint32_t kBase = 0x64006400u;  // 1024
+// The four nibbles of each half of w as fp16 pairs c - Z (Z = 8 or 7): even ones sit in bits 0-3,
+// odd ones in bits 4-7 of each half of w or of w >> 8.
+template <int Z>
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&a)[4]) {
+  constexpr uint32_t kBase = 0x64006400u;                             // 1024
+  constexpr uint32_t kEven = Z == 8 ? 0xe408e408u : 0xe407e407u;      // - (1024 + Z)
+  constexpr uint32_t kOdd = Z == 8 ? 0xd480d480u : 0xd470d470u;       // - (64 + Z), after / 16
   const uint32_t w8 = w >> 8;
-  a[0] = h2_add(and_or(w, 0x000f000fu, kBase), 0xe408e408u);                // - 1032
-  a[1] = h2_fma(and_or(w, 0x00f000f0u, kBase), 0x2c002c00u, 0xd480d480u);   // / 16 - 72
-  a[2] = h2_add(and_or(w8, 0x000f000fu, kBase), 0xe408e408u);
-  a[3] = h2_fma(and_or(w8, 0x00f000f0u, kBase), 0x2c002c00u, 0xd480d480u);
-}
-// The same as c - 7.5, the nibbles one bit further up in the mantissa of 512.
-__device__ __forceinline__ void v_codes(uint32_t w, uint32_t (&a)[4]) {
-  constexpr uint32_t kBase = 0x60006000u;  // 512
-  const uint32_t w1 = w << 1, w7 = w >> 7;
-  a[0] = h2_add(and_or(w1, 0x001e001eu, kBase), 0xe00fe00fu);               // - 519.5
-  a[1] = h2_fma(and_or(w1, 0x01e001e0u, kBase), 0x2c002c00u, 0xd0f0d0f0u);  // / 16 - 39.5
-  a[2] = h2_add(and_or(w7, 0x001e001eu, kBase), 0xe00fe00fu);
-  a[3] = h2_fma(and_or(w7, 0x01e001e0u, kBase), 0x2c002c00u, 0xd0f0d0f0u);
+  a[0] = h2_add(and_or(w, 0x000f000fu, kBase), kEven);
+  a[1] = h2_fma(and_or(w, 0x00f000f0u, kBase), 0x2c002c00u, kOdd);
+  a[2] = h2_add(and_or(w8, 0x000f000fu, kBase), kEven);
+  a[3] = h2_fma(and_or(w8, 0x00f000f0u, kBase), 0x2c002c00u, kOdd);
 }
 
-// Lane roles. gid = lane / 4, tig = lane % 4. A step takes kPages pages. For the softmax a lane
-// holds two tokens, gid and gid + 8 of its page, of one head: with four heads per KV head the
-// columns are (group, head) and lanes tig, tig ^ 2 hold the two groups of a head pair; with two
-// (or one, the second idle) the columns are held twice, tig / 2 picks the page and tig ^ 1 is the
-// other group. For P.V a lane holds dims 64 g + 8 gid .. + 7 of both groups of head tig.
+// Lane roles. gid = lane / 4, tig = lane % 4. A step takes kPages pages. The accumulator columns are
+// (head, group), so lane tig holds both groups of head tig of tokens gid and gid + 8 and forms their
+// scores by itself; with fewer than four heads per KV head the columns are held twice and tig / 2
+// picks the page (with one, the second head is idle). For P.V the lane holds dims 64 g + 8 gid .. + 7 of
+// both groups of the same head.
 template <int G>
 struct Roles {
   static constexpr int kHeads = G == 4 ? 4 : 2;
   static constexpr int kPages = G == 4 ? 1 : 2;
-  static constexpr int kOther = G == 4 ? 2 : 1;  // lane xor that holds the other group
-  __device__ static int group(int tig) { return (tig & kOther) ? 1 : 0; }
-  __device__ static int head(int tig) { return G == 4 ? 2 * (tig & 1) + (tig >> 1) : (tig & 1); }
+  __device__ static int head(int tig) { return tig & (kHeads - 1); }
   __device__ static int page(int tig) { return G == 4 ? 0 : (tig >> 1); }
-  // tig of a lane whose softmax head is the P.V head of lane tig
-  __device__ static int owner(int tig) { return G == 4 ? ((tig >> 1) | ((tig & 1) << 1)) : (tig & 1); }
 };
 
 struct Kv4State {
   float m, l;          // running maximum (base 2) and this lane's part of the softmax sum
-  float corr[2];       // this lane's part of sum w (M_g + 7.5 S_g)
+  float corr[2];       // this lane's part of sum w (M_g + z S_g)
   float r[2];          // w S_g enters the tensor cores times this power of two
   float acc[8][4];     // tile 4 g + j: dims 64 g + 8 gid + j (0, 1) and + j + 4 (2, 3); columns
-};                     // 2 tig, 2 tig + 1 are the two parts of head tig
+};                     // 2 tig, 2 tig + 1 are the two parts of the head
 
 constexpr float kR0 = 1.2676506e30f;   // 2^100
 constexpr float kNoMax = -1e30f;       // running maximum before any visible score
 
-// The group's q as B fragments and per-column sums. Returns the power of two that undoes q's.
+// The group's q as B fragments and, for the lane's own head, sum q of each group and the factor that
+// undoes q's power of two. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
+// word e = s / 2 of the lane's 16-byte code chunk, which is all group e & 1.
 template <int G>
 __device__ __forceinline__ float load_q4(const __nv_bfloat16* q, int lane, uint32_t (&b)[8][2],
                                          float (&qs)[2]) {
   using R = Roles<G>;
   const int gid = lane >> 2, tig = lane & 3;
-  const int grp = G == 4 ? gid >> 2 : (gid >> 1) & 1;
-  const int head = G == 4 ? gid & 3 : gid & 1;
-  float x[32];  // column gid's dims of this lane's 16-byte code chunk, in word order
-  float top = 0.f, sum = 0.f;
+  const int head = (gid >> 1) & (R::kHeads - 1), grp = gid & 1;
+  float x[4][8];
+  float top = 0.f, sum[2] = {0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (head < G && (e & 1) == grp)
+    if (head < G)
       v = *reinterpret_cast<const uint4*>(q + head * kHeadDim + 64 * (e & 1) + 8 * (2 * tig + (e >> 1)));
-    float f[8];
-    unpack8(v, f);
+    unpack8(v, x[e]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      x[8 * e + k] = f[k];
-      top = fmaxf(top, fabsf(f[k]));
-      sum += f[k];
+      top = fmaxf(top, fabsf(x[e][k]));
+      sum[e & 1] += x[e][k];
     }
   }
-  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  qs[0] = __shfl_sync(0xffffffffu, sum, 8 * tig);
-  qs[1] = __shfl_sync(0xffffffffu, sum, 8 * tig + 4);
-  const uint32_t ebits = __reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23;
-  const uint32_t f = min(268u - min(ebits, 254u), 253u);  // largest |q| to [2^14, 2^15)
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+    sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
+  }
+  const uint32_t f = min(268u - min(__float_as_uint(top) >> 23, 254u), 253u);  // |q| below 2^15
   const float up = __uint_as_float(f << 23);
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
     const int e = s >> 1, j = 2 * (s & 1);
-    b[s][0] = h2_pack(x[8 * e + j] * up, x[8 * e + j + 4] * up);
-    b[s][1] = h2_pack(x[8 * e + j + 1] * up, x[8 * e + j + 5] * up);
+    const bool mine = (e & 1) == grp;
+    b[s][0] = mine ? h2_pack(x[e][j] * up, x[e][j + 4] * up) : 0u;
+    b[s][1] = mine ? h2_pack(x[e][j + 1] * up, x[e][j + 5] * up) : 0u;
   }
-  return __uint_as_float((254u - f) << 23);
+  const int src = 8 * R::head(tig);  // a lane whose column is the lane's head
+  qs[0] = __shfl_sync(0xffffffffu, sum[0], src);
+  qs[1] = __shfl_sync(0xffffffffu, sum[1], src);
+  return __uint_as_float((254u - __shfl_sync(0xffffffffu, f, src)) << 23);
 }
 
 // A page of a warp's share: where it lies and which of its rows count.
@@ -206,9 +200,9 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
   using R = Roles<G>;
   constexpr int NP = R::kPages, HG = R::kHeads;
   const int gid = lane >> 2, tig = lane & 3;
-  const int mygrp = R::group(tig), myhead = R::head(tig), mypage = R::page(tig);
+  const int myhead = R::head(tig), mypage = R::page(tig);
 
-  // ---- scores: c[page][token gid: 0, 1; gid + 8: 2, 3][columns 2 tig, 2 tig + 1] ----
+  // ---- sums c[page]: token gid groups 0, 1; token gid + 8 groups 0, 1 ----
   float c[NP][4];
   const unsigned char* kbase = stage + gid * kKv4RowBytes + 16 * tig;
 #pragma unroll
@@ -221,8 +215,8 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t ca[4], cb[4];
-      k_codes(a[e], ca);
-      k_codes(b[e], cb);
+      codes_f16<8>(a[e], ca);
+      codes_f16<8>(b[e], cb);
       mma_16816_f16(c[n], ca[0], cb[0], ca[1], cb[1], qb[2 * e][0], qb[2 * e][1]);
       mma_16816_f16(c[n], ca[2], cb[2], ca[3], cb[3], qb[2 * e + 1][0], qb[2 * e + 1][1]);
     }
@@ -230,17 +224,16 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
   const unsigned char* mbase = stage + mypage * kKv4PageBytes + kKv4MetaOff + gid * kKv4MetaBytes;
   uint4 ma = *reinterpret_cast<const uint4*>(mbase);
   uint4 mb = *reinterpret_cast<const uint4*>(mbase + 8 * kKv4MetaBytes);
-  float cc[4];
+  float x0 = 0.f, x1 = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) cc[i] = (NP == 2 && mypage) ? c[NP - 1][i] : c[0][i];
-  const uint32_t ka = mygrp ? ma.y : ma.x, kb = mygrp ? mb.y : mb.x;
-  const float sa = kv4_scale(ka), sb = kv4_scale(kb);
-  const float za = fmaf(8.f, sa, kv4_min(ka)), zb = fmaf(8.f, sb, kv4_min(kb));
-  const float s00 = fmaf(sa * kq, cc[0], za * qs[0]), s01 = fmaf(sa * kq, cc[1], za * qs[1]);
-  const float s10 = fmaf(sb * kq, cc[2], zb * qs[0]), s11 = fmaf(sb * kq, cc[3], zb * qs[1]);
-  // keep the head this lane owns, trade the other's partial sums for the missing group's
-  float x0 = (mygrp ? s01 : s00) + __shfl_xor_sync(0xffffffffu, mygrp ? s00 : s01, R::kOther);
-  float x1 = (mygrp ? s11 : s10) + __shfl_xor_sync(0xffffffffu, mygrp ? s10 : s11, R::kOther);
+  for (int g = 0; g < 2; ++g) {
+    const float c0 = (NP == 2 && mypage) ? c[NP - 1][g] : c[0][g];
+    const float c1 = (NP == 2 && mypage) ? c[NP - 1][2 + g] : c[0][2 + g];
+    const uint32_t ka = g ? ma.y : ma.x, kb = g ? mb.y : mb.x;
+    const float sa = kv4_scale(ka), sb = kv4_scale(kb);
+    x0 = fmaf(sa * kq, c0, fmaf(fmaf(8.f, sa, kv4_min(ka)), qs[g], x0));
+    x1 = fmaf(sb * kq, c1, fmaf(fmaf(8.f, sb, kv4_min(kb)), qs[g], x1));
+  }
 
   const int mine = (NP == 2 && mypage) ? entry[NP - 1] : entry[0];
   bool v0 = true, v1 = true;
@@ -280,23 +273,23 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
     st.l *= al;
     st.corr[0] *= al;
     st.corr[1] *= al;
-    const float ah = __shfl_sync(0xffffffffu, al, (lane & ~3) | R::owner(tig));
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st.acc[t][i] *= ah;
+      for (int i = 0; i < 4; ++i) st.acc[t][i] *= al;
   }
   const float p0 = ex2_fast(x0 - st.m), p1 = ex2_fast(x1 - st.m);
   st.l += p0 + p1;
 
   // ---- weights times the V scales, as two fp16 each ----
   const uint32_t va[2] = {ma.z, ma.w}, vb[2] = {mb.z, mb.w};
+  const float z = (gid & 4) ? 7.f : 8.f;  // what P.V subtracts from this lane's tokens' codes
   float y0[2], y1[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const float s0 = kv4_scale(va[g]), s1 = kv4_scale(vb[g]);
-    st.corr[g] = fmaf(p0, fmaf(7.5f, s0, kv4_min(va[g])), st.corr[g]);
-    st.corr[g] = fmaf(p1, fmaf(7.5f, s1, kv4_min(vb[g])), st.corr[g]);
+    st.corr[g] = fmaf(p0, fmaf(z, s0, kv4_min(va[g])), st.corr[g]);
+    st.corr[g] = fmaf(p1, fmaf(z, s1, kv4_min(vb[g])), st.corr[g]);
     y0[g] = p0 * s0;
     y1[g] = p1 * s1;
   }
@@ -317,11 +310,10 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
         ratio = rn / st.r[g];
         st.r[g] = rn;
       }
-      const float rh = __shfl_sync(0xffffffffu, ratio, (lane & ~3) | R::owner(tig));
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st.acc[4 * g + j][i] *= rh;
+        for (int i = 0; i < 4; ++i) st.acc[4 * g + j][i] *= ratio;
     }
   }
   uint32_t hi[2], lo[2];
@@ -353,10 +345,10 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
       const uint32_t u0 = g ? w0.y : w0.x, u1 = g ? w1.y : w1.x;
       const uint32_t u2 = g ? w2.y : w2.x, u3 = g ? w3.y : w3.x;
       uint32_t a0[4], a1[4], a2[4], a3[4];
-      v_codes(__byte_perm(u0, u1, 0x5410), a0);
-      v_codes(__byte_perm(u0, u1, 0x7632), a1);
-      v_codes(__byte_perm(u2, u3, 0x5410), a2);
-      v_codes(__byte_perm(u2, u3, 0x7632), a3);
+      codes_f16<8>(__byte_perm(u0, u1, 0x5410), a0);  // tokens tig, tig + 8
+      codes_f16<8>(__byte_perm(u0, u1, 0x7632), a1);
+      codes_f16<7>(__byte_perm(u2, u3, 0x5410), a2);  // tokens tig + 4, tig + 12
+      codes_f16<7>(__byte_perm(u2, u3, 0x7632), a3);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         mma_16816_f16(st.acc[4 * g + j], a0[j], a1[j], a2[j], a3[j], g ? b0.y : b0.x, g ? b1.y : b1.x);
@@ -614,21 +606,15 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
       Lw[warp * HG + R::head(tig)] = st.l;
     }
     {
-      const int src = (lane & ~3) | R::owner(tig);
-      float corr[2], inv[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        corr[i] = __shfl_sync(0xffffffffu, st.corr[i], src);
-        inv[i] = 1.f / __shfl_sync(0xffffffffu, st.r[i], src);
-      }
       if (tig < HG) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          const float inv = 1.f / st.r[i];
           float o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            o[j] = fmaf(st.acc[4 * i + j][0] + st.acc[4 * i + j][1], inv[i], corr[i]);
-            o[j + 4] = fmaf(st.acc[4 * i + j][2] + st.acc[4 * i + j][3], inv[i], corr[i]);
+            o[j] = fmaf(st.acc[4 * i + j][0] + st.acc[4 * i + j][1], inv, st.corr[i]);
+            o[j + 4] = fmaf(st.acc[4 * i + j][2] + st.acc[4 * i + j][3], inv, st.corr[i]);
           }
           float4* dst = reinterpret_cast<float4*>(Aw + (warp * HG + tig) * kHeadDim + 64 * i + 8 * gid);
           dst[0] = make_float4(o[0], o[1], o[2], o[3]);
