@@ -32,12 +32,14 @@ namespace oda {
 
 constexpr int kW4 = 8;               // warps per CTA
 constexpr int kThreads4 = kW4 * 32;
-constexpr int kSlots4 = 4;           // pages a warp holds in shared memory
+constexpr int kPages4 = 2;           // pages a step takes
+constexpr int kStages4 = 2;          // steps a warp holds in shared memory: one in use, one coming
+constexpr int kStageBytes4 = kPages4 * kKv4PageBytes;
 constexpr int kRefs4 = 64;           // page references a warp holds (two halves, refilled in turn)
 constexpr int kCtasPerSm4 = 2;
 constexpr int kMinShare4 = 8;        // units per CTA at least (one page per warp)
 constexpr int kPStride = 48;         // words per (page, head) of the weight exchange
-constexpr int kPWords = 4 * kPStride;
+constexpr int kPWords = 2 * 4 * kPStride;
 
 struct Kv4Params {
   PlanArgs plan;
@@ -57,8 +59,6 @@ struct Kv4Params {
   unsigned int* ws_ticket;
   int* status;
   unsigned long long* stats;
-  unsigned long long wait_ns;
-  int test_stall;
 };
 
 __device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -108,15 +108,15 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&a)[4]) {
   a[3] = h2_fma(and_or(w8, 0x00f000f0u, kBase), 0x2c002c00u, kOdd);
 }
 
-// Lane roles. gid = lane / 4, tig = lane % 4. A step takes kPages pages. The accumulator columns are
+// Lane roles. gid = lane / 4, tig = lane % 4. A step takes two pages. The accumulator columns are
 // (head, group), so lane tig holds both groups of head tig of tokens gid and gid + 8 and forms their
-// scores by itself; with fewer than four heads per KV head the columns are held twice and tig / 2
-// picks the page (with one, the second head is idle). For P.V the lane holds dims 64 g + 8 gid .. + 7 of
-// both groups of the same head.
+// scores by itself. With four heads per KV head it does so for both pages; with fewer the columns are
+// held twice and tig / 2 picks the page (with one head, the second is idle). For P.V the lane holds
+// dims 64 g + 8 gid .. + 7 of both groups of the same head.
 template <int G>
 struct Roles {
   static constexpr int kHeads = G == 4 ? 4 : 2;
-  static constexpr int kPages = G == 4 ? 1 : 2;
+  static constexpr int kMine = G == 4 ? 2 : 1;  // pages whose scores a lane holds
   __device__ static int head(int tig) { return tig & (kHeads - 1); }
   __device__ static int page(int tig) { return G == 4 ? 0 : (tig >> 1); }
 };
@@ -175,11 +175,12 @@ __device__ __forceinline__ float load_q4(const __nv_bfloat16* q, int lane, uint3
   return __uint_as_float((254u - __shfl_sync(0xffffffffu, f, src)) << 23);
 }
 
-// A page of a warp's share: where it lies and which of its rows count.
-struct PageEntry {
-  int pos;   // first position + visible rows - 1 (a page's first position is a multiple of 16);
-             // negative: nothing to read (past the share's end, or reported)
-  int page;  // physical page
+// The pages of a warp's share. pos: first position + visible rows - 1 (a page's first position is a
+// multiple of 16); negative: nothing to attend (past the share's end, or a bad page, reported). src: what to copy
+// (for such a page the cache's first, which nothing of counts).
+struct PageRefs {
+  const unsigned char* src[kRefs4];
+  int pos[kRefs4];
 };
 
 // Visible rows among the 16 positions from `pos`.
@@ -189,24 +190,23 @@ __device__ __forceinline__ int rows_in_page(const SeqPlan& s, int pos) {
   return max(0, hi - lo + 1) - max(0, ghi - glo + 1);
 }
 
-// One step over the kPages pages at `stage` (a page that is not there holds stale bytes: its codes
-// are finite numbers whatever they are, its scales and minima are not used). entry[n] as above. kq
-// undoes q's power of two and carries the softmax scale in base 2; qs is sum q times that scale.
+// One step over the two pages at `stage` (of a page with a negative entry no scale or minimum is used;
+// its codes are finite numbers whatever they are). kq undoes q's power of two and carries the softmax
+// scale in base 2; qs is sum q times that scale.
 template <int G, bool kScores>
-__device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (&entry)[Roles<G>::kPages],
-                                         const SeqPlan& sp, const uint32_t (&qb)[8][2], float kq,
-                                         const float (&qs)[2], Kv4State& st, uint32_t* pw,
-                                         float* scores, int cap, int lane) {
+__device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry, const SeqPlan& sp,
+                                         const uint32_t (&qb)[8][2], float kq, const float (&qs)[2],
+                                         Kv4State& st, uint32_t* pw, float* scores, int cap, int lane) {
   using R = Roles<G>;
-  constexpr int NP = R::kPages, HG = R::kHeads;
+  constexpr int NM = R::kMine, HG = R::kHeads;
   const int gid = lane >> 2, tig = lane & 3;
   const int myhead = R::head(tig), mypage = R::page(tig);
 
   // ---- sums c[page]: token gid groups 0, 1; token gid + 8 groups 0, 1 ----
-  float c[NP][4];
+  float c[2][4];
   const unsigned char* kbase = stage + gid * kKv4RowBytes + 16 * tig;
 #pragma unroll
-  for (int n = 0; n < NP; ++n) {
+  for (int n = 0; n < 2; ++n) {
     const uint4 wa = *reinterpret_cast<const uint4*>(kbase + n * kKv4PageBytes);
     const uint4 wb = *reinterpret_cast<const uint4*>(kbase + n * kKv4PageBytes + 8 * kKv4RowBytes);
     const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
@@ -221,52 +221,65 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
       mma_16816_f16(c[n], ca[2], cb[2], ca[3], cb[3], qb[2 * e + 1][0], qb[2 * e + 1][1]);
     }
   }
-  const unsigned char* mbase = stage + mypage * kKv4PageBytes + kKv4MetaOff + gid * kKv4MetaBytes;
-  uint4 ma = *reinterpret_cast<const uint4*>(mbase);
-  uint4 mb = *reinterpret_cast<const uint4*>(mbase + 8 * kKv4MetaBytes);
-  float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const float c0 = (NP == 2 && mypage) ? c[NP - 1][g] : c[0][g];
-    const float c1 = (NP == 2 && mypage) ? c[NP - 1][2 + g] : c[0][2 + g];
-    const uint32_t ka = g ? ma.y : ma.x, kb = g ? mb.y : mb.x;
-    const float sa = kv4_scale(ka), sb = kv4_scale(kb);
-    x0 = fmaf(sa * kq, c0, fmaf(fmaf(8.f, sa, kv4_min(ka)), qs[g], x0));
-    x1 = fmaf(sb * kq, c1, fmaf(fmaf(8.f, sb, kv4_min(kb)), qs[g], x1));
-  }
 
-  const int mine = (NP == 2 && mypage) ? entry[NP - 1] : entry[0];
-  bool v0 = true, v1 = true;
-  const bool part = NP == 2 ? ((entry[0] & entry[NP - 1]) & 15) != 15 || (entry[0] | entry[NP - 1]) < 0
-                            : (entry[0] & 15) != 15 || entry[0] < 0;
-  if (part) {  // (uniform) some row of these pages is hidden or absent: nothing of it may count
-    const int pos = mine & ~15;
-    v0 = mine >= 0 && row_visible(sp, pos + gid);
-    v1 = mine >= 0 && row_visible(sp, pos + gid + 8);
-    if (!v0) {
-      x0 = -INFINITY;
-      ma.z = ma.w = 0u;
+  // ---- this lane's scores x[page][token gid, gid + 8] and the V meta of those tokens ----
+  const unsigned char* mbase = stage + mypage * kKv4PageBytes + kKv4MetaOff + gid * kKv4MetaBytes;
+  float x[NM][2];
+  uint32_t vm[NM][2][2];  // [page][token][group]
+#pragma unroll
+  for (int n = 0; n < NM; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 m = *reinterpret_cast<const uint4*>(mbase + n * kKv4PageBytes + 8 * i * kKv4MetaBytes);
+      vm[n][i][0] = m.z;
+      vm[n][i][1] = m.w;
+      x[n][i] = 0.f;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float cc = (NM == 1 && mypage) ? c[1][2 * i + g] : c[n][2 * i + g];
+        const uint32_t km = g ? m.y : m.x;
+        const float s = kv4_scale(km);
+        x[n][i] = fmaf(s * kq, cc, fmaf(fmaf(8.f, s, kv4_min(km)), qs[g], x[n][i]));
+      }
     }
-    if (!v1) {
-      x1 = -INFINITY;
-      mb.z = mb.w = 0u;
+
+  const bool whole = (entry.x & entry.y & 15) == 15 && (entry.x | entry.y) >= 0;
+  if (!whole) {  // (uniform) some row of these pages is hidden or absent: nothing of it may count
+#pragma unroll
+    for (int n = 0; n < NM; ++n) {
+      const int mine = (NM == 2 ? n : mypage) ? entry.y : entry.x;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (mine < 0 || !row_visible(sp, (mine & ~15) + gid + 8 * i)) {
+          x[n][i] = -INFINITY;
+          vm[n][i][0] = vm[n][i][1] = 0u;
+        }
     }
   }
   if constexpr (kScores) {
     if (myhead < G) {
-      float* dst = scores + (size_t)myhead * cap + (mine & ~15);
-      if (v0) dst[gid] = x0;
-      if (v1) dst[gid + 8] = x1;
+#pragma unroll
+      for (int n = 0; n < NM; ++n) {
+        const int mine = (NM == 2 ? n : mypage) ? entry.y : entry.x;
+        float* dst = scores + (size_t)myhead * cap + (mine & ~15) + gid;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)  // (what hides a row is looked up again: a score may be -inf)
+          if (whole || (mine >= 0 && row_visible(sp, (mine & ~15) + gid + 8 * i))) dst[8 * i] = x[n][i];
+      }
     }
   }
 
   // ---- online softmax; the maximum is raised only when a score passes it by 2^kLazyMax ----
-  if (__any_sync(0xffffffffu, fmaxf(x0, x1) > st.m + kLazyMax)) {
-    float mx = fmaxf(x0, x1);
-    if (NP == 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+  auto over_head = [&](float v) {  // maximum over the lanes that hold the head
+    if (NM == 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+  };
+  float top = fmaxf(x[0][0], x[0][1]);
+  if (NM == 2) top = fmaxf(top, fmaxf(x[NM - 1][0], x[NM - 1][1]));
+  if (__any_sync(0xffffffffu, top > st.m + kLazyMax)) {
+    const float mx = over_head(top);
     const bool up = mx > st.m + kLazyMax;
     const float al = up ? ex2_fast(st.m - mx) : 1.f;
     if (up) st.m = mx;
@@ -278,32 +291,33 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.acc[t][i] *= al;
   }
-  const float p0 = ex2_fast(x0 - st.m), p1 = ex2_fast(x1 - st.m);
-  st.l += p0 + p1;
 
-  // ---- weights times the V scales, as two fp16 each ----
-  const uint32_t va[2] = {ma.z, ma.w}, vb[2] = {mb.z, mb.w};
+  // ---- weights times the V scales ----
   const float z = (gid & 4) ? 7.f : 8.f;  // what P.V subtracts from this lane's tokens' codes
-  float y0[2], y1[2];
+  float y[NM][2][2];                      // [page][group][token]
+#pragma unroll
+  for (int n = 0; n < NM; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float w = ex2_fast(x[n][i] - st.m);
+      st.l += w;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float s = kv4_scale(vm[n][i][g]);
+        st.corr[g] = fmaf(w, fmaf(z, s, kv4_min(vm[n][i][g])), st.corr[g]);
+        y[n][g][i] = w * s;
+      }
+    }
+  float ymax[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const float s0 = kv4_scale(va[g]), s1 = kv4_scale(vb[g]);
-    st.corr[g] = fmaf(p0, fmaf(z, s0, kv4_min(va[g])), st.corr[g]);
-    st.corr[g] = fmaf(p1, fmaf(z, s1, kv4_min(vb[g])), st.corr[g]);
-    y0[g] = p0 * s0;
-    y1[g] = p1 * s1;
+    ymax[g] = fmaxf(y[0][g][0], y[0][g][1]);
+    if (NM == 2) ymax[g] = fmaxf(ymax[g], fmaxf(y[NM - 1][g][0], y[NM - 1][g][1]));
   }
-  bool high = false;
-#pragma unroll
-  for (int g = 0; g < 2; ++g) high |= fmaxf(y0[g], y1[g]) * st.r[g] > 32768.f;
-  if (__any_sync(0xffffffffu, high)) {
+  if (__any_sync(0xffffffffu, fmaxf(ymax[0] * st.r[0], ymax[1] * st.r[1]) > 32768.f)) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      float ym = fmaxf(y0[g], y1[g]);
-      if (NP == 2) ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 2));
-      ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 4));
-      ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 8));
-      ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, 16));
+      const float ym = over_head(ymax[g]);
       float ratio = 1.f;
       if (ym * st.r[g] > 32768.f) {  // the largest weight to [2^7, 2^8)
         const float rn = __uint_as_float((261u - min(__float_as_uint(ym) >> 23, 254u)) << 23);
@@ -316,22 +330,26 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
         for (int i = 0; i < 4; ++i) st.acc[4 * g + j][i] *= ratio;
     }
   }
-  uint32_t hi[2], lo[2];
+  // as two fp16 each
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const float w0 = y0[g] * st.r[g], w1 = y1[g] * st.r[g];
-    hi[g] = h2_pack(w0, w1);
-    const float2 f = h2_unpack(hi[g]);
-    lo[g] = h2_pack(w0 - f.x, w1 - f.y);
+  for (int n = 0; n < NM; ++n) {
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const float w0 = y[n][g][0] * st.r[g], w1 = y[n][g][1] * st.r[g];
+      hi[g] = h2_pack(w0, w1);
+      const float2 f = h2_unpack(hi[g]);
+      lo[g] = h2_pack(w0 - f.x, w1 - f.y);
+    }
+    *reinterpret_cast<uint4*>(pw + ((mypage + n) * HG + myhead) * kPStride + 4 * gid) =
+        make_uint4(hi[0], hi[1], lo[0], lo[1]);
   }
-  *reinterpret_cast<uint4*>(pw + (mypage * HG + myhead) * kPStride + 4 * gid) =
-      make_uint4(hi[0], hi[1], lo[0], lo[1]);
   __syncwarp();
 
   // ---- P.V ----
   const int bh = (gid >> 1) & (HG - 1), col = gid & 1;
 #pragma unroll
-  for (int n = 0; n < NP; ++n) {
+  for (int n = 0; n < 2; ++n) {
     const uint32_t* src = pw + (n * HG + bh) * kPStride + 2 * col;
     const uint2 b0 = *reinterpret_cast<const uint2*>(src + 4 * tig);
     const uint2 b1 = *reinterpret_cast<const uint2*>(src + 4 * (tig + 4));
@@ -354,7 +372,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, const int (
         mma_16816_f16(st.acc[4 * g + j], a0[j], a1[j], a2[j], a3[j], g ? b0.y : b0.x, g ? b1.y : b1.x);
     }
   }
-  __syncwarp();  // the exchange area is written again by the next step
+  __syncwarp();  // the stage and the exchange area may be written again
 }
 
 __device__ __forceinline__ void kv4_write(const Kv4Params& p, int b, int h, int dim, float o, float l2) {
@@ -368,37 +386,53 @@ __device__ __forceinline__ void kv4_write(const Kv4Params& p, int b, int h, int 
 }
 
 struct Kv4Smem {
-  static constexpr int kSlotsOff = 0;
-  static constexpr int kBarsOff = kW4 * kSlots4 * kKv4PageBytes;
-  static constexpr int kPOff = kBarsOff + (kW4 * kSlots4 * 8 + 15) / 16 * 16;
+  static constexpr int kPOff = kW4 * kStages4 * kStageBytes4;
   static constexpr int kRefOff = kPOff + kW4 * kPWords * 4;
-  static constexpr int kPreOff = kRefOff + kW4 * kRefs4 * (int)sizeof(PageEntry);
+  static constexpr int kPreOff = kRefOff + kW4 * (int)sizeof(PageRefs);
   static constexpr int kBytes = kPreOff + (kMaxBatch + 1) * 4;
 };
+
+// Copy a step's two pages into its stage: 288 16-byte pieces, nine a lane, as one group of copies.
+// (One bulk copy a page costs a warp more instructions than these nine: the engine's operands are
+// uniform registers. Measured on a 128K history: 41.1 us with bulk copies.)
+__device__ __forceinline__ void kv4_copy(uint32_t dst, const unsigned char* a, const unsigned char* b,
+                                         int lane, uint64_t policy) {
+  constexpr int kPieces = kKv4PageBytes / 16;
+  static_assert(2 * kPieces == 9 * 32, "nine pieces a lane");
+  const unsigned char* pa = a + 16 * lane;
+  const unsigned char* pb = b + 16 * lane - kKv4PageBytes;  // piece 144 is the second page's first
+  dst += 16 * lane;
+#pragma unroll
+  for (int k = 0; k < 9; ++k) {
+    const unsigned char* src = k < 4 ? pa : k > 4 ? pb : lane < kPieces - 128 ? pa : pb;
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst + 512 * k),
+                 "l"(src + 512 * k), "l"(policy)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 template <int G, bool kScores>
 __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(const Kv4Params p) {
   using R = Roles<G>;
-  constexpr int NP = R::kPages, HG = R::kHeads;
+  constexpr int HG = R::kHeads;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_align, s_last;
   __shared__ unsigned long long s_rows, s_pages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  unsigned char* slots = smem + Kv4Smem::kSlotsOff + warp * kSlots4 * kKv4PageBytes;
-  constexpr int kStages = kSlots4 / NP;  // of NP pages, one barrier each
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Kv4Smem::kBarsOff) + warp * kSlots4;
-  PageEntry* refs = reinterpret_cast<PageEntry*>(smem + Kv4Smem::kRefOff) + warp * kRefs4;
+  unsigned char* stages = smem + warp * kStages4 * kStageBytes4;
   uint32_t* pw = reinterpret_cast<uint32_t*>(smem + Kv4Smem::kPOff) + warp * kPWords;
+  PageRefs& refs = reinterpret_cast<PageRefs*>(smem + Kv4Smem::kRefOff)[warp];
   int* pre = reinterpret_cast<int*>(smem + Kv4Smem::kPreOff);
   const int B = p.batch, Hkv = p.hkv;
   const int P = gridDim.x, cta = blockIdx.x;
 
   // ---- prefix of visible units per sequence, share alignment ----
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&bars[s], NP);
-    fence_barrier_init();
-  }
   if (tid == 0) {
     s_rows = 0;
     s_pages = 0;
@@ -444,8 +478,6 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     else if (Pe >= s_align) Pe -= Pe % s_align;
   }
   const uint64_t policy = l2_evict_first_policy();
-  unsigned wcount = 0;  // stages this warp has used
-  bool dead = false;
   long long x = cta < Pe ? (T * cta) / Pe : 0;
   const long long x_end = cta < Pe ? (T * (cta + 1)) / Pe : 0;
   while (x < x_end) {
@@ -465,53 +497,43 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     const SeqPlan sp = make_plan(p.plan, b);
     const int bg = b * Hkv + g;
 
-    // this warp's pages: runs of NP consecutive list entries, strided over the warps
-    const int steps = (j1 - j0 + NP - 1) / NP;
-    const int my_steps = steps > warp ? (steps - warp + kW4 - 1) / kW4 : 0;
-    // page n of this warp is list entry j0 + (n / NP * kW4 + warp) * NP + n % NP
+    // this warp's steps: pairs of consecutive list entries, strided over the warps
+    const int pairs = (j1 - j0 + 1) / 2;
+    const int steps = pairs > warp ? (pairs - warp + kW4 - 1) / kW4 : 0;
     unsigned rows_vis = 0, pages_read = 0;  // this lane's pages
-    auto fill = [&](int n0) {  // references of pages n0 .. n0 + 31
+    auto fill = [&](int n0) {  // references of pages n0 .. n0 + 31; page n is entry n % 2 of step n / 2
       const int n = n0 + lane;
-      const int j = j0 + ((n / NP) * kW4 + warp) * NP + n % NP;
-      PageEntry e;
-      e.pos = -1;
-      e.page = 0;
-      if (n < my_steps * NP && j < j1) {
+      const int j = j0 + ((n >> 1) * kW4 + warp) * 2 + (n & 1);
+      int pos = -1;
+      const unsigned char* src = p.cache;
+      if ((n >> 1) < steps && j < j1) {
         const PageRef r = page_ref(p.plan, sp, b, j);
         if (r.err != 0) {
           report(p.status, r.err);
         } else {
           const int rows = rows_in_page(sp, r.lp * kPage);
-          if (rows > 0) e.pos = r.lp * kPage + rows - 1;
-          e.page = r.pb;
+          if (rows > 0) pos = r.lp * kPage + rows - 1;
+          src = p.cache + ((size_t)r.pb * Hkv + g) * kKv4PageBytes;
           rows_vis += rows;
           ++pages_read;
         }
       }
-      refs[n % kRefs4] = e;
+      refs.pos[n % kRefs4] = pos;
+      refs.src[n % kRefs4] = src;
     };
-    auto issue = [&](int step) {  // lanes below NP: bring a step's pages into its stage
-      const PageEntry e = refs[(step * NP + lane) % kRefs4];
-      const unsigned k = wcount + step;
-      uint64_t* bar = &bars[k % kStages];
-      if (p.test_stall == 1 && cta == 0 && warp == 0 && k == 0) {
-        mbar_arrive_expect_tx(bar, 16u);  // test hook: bytes that never arrive
-      } else if (e.pos >= 0) {
-        mbar_arrive_expect_tx(bar, kKv4PageBytes);
-        bulk_load(slots + ((k % kStages) * NP + lane) * kKv4PageBytes,
-                  p.cache + ((size_t)e.page * Hkv + g) * kKv4PageBytes, kKv4PageBytes, bar, policy);
-      } else {
-        mbar_arrive(bar);
+    auto issue = [&](int s) {  // one group of copies a step, empty past the last
+      if (s < steps) {
+        const ulonglong2 src = *reinterpret_cast<const ulonglong2*>(&refs.src[2 * s % kRefs4]);
+        kv4_copy(smem_addr(stages) + (s & 1) * kStageBytes4, reinterpret_cast<const unsigned char*>(src.x),
+                 reinterpret_cast<const unsigned char*>(src.y), lane, policy);
       }
+      copies_commit();
     };
-    if (!dead) {
-      fill(0);
-      if (my_steps * NP > 32) fill(32);
-      __syncwarp();
-      if (lane < NP)
-        for (int s = 0; s < min(my_steps, kStages); ++s) issue(s);
-    }
+    fill(0);
+    if (steps > 16) fill(32);
     __syncwarp();
+    issue(0);
+    issue(1);
 
     uint32_t qb[8][2];
     float qs[2];
@@ -531,45 +553,32 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.acc[t][i] = 0.f;
 
-    for (int s = 0; s < my_steps && !dead; ++s) {
-      if (s > 0 && s % (32 / NP) == 0 && s * NP + 32 < my_steps * NP) {
-        fill(s * NP + 32);  // the half that was used up last
-        __syncwarp();
-      }
-      const unsigned k = wcount + s;
-      unsigned char* stage = slots + (k % kStages) * NP * kKv4PageBytes;
-      int entry[NP];
-#pragma unroll
-      for (int i = 0; i < NP; ++i) entry[i] = refs[(s * NP + i) % kRefs4].pos;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars[k % kStages], (k / kStages) & 1u, p.wait_ns))) {
-        if (lane == 0) report(p.status, ODA_DEV_TIMEOUT);
-        // let the copies already started into the other stages land, then stop
-        for (int m = s + 1; m < min(my_steps, s + kStages); ++m)
-          mbar_wait(&bars[(wcount + m) % kStages], ((wcount + m) / kStages) & 1u, p.wait_ns);
-        dead = true;
-        break;
-      }
+    for (int s = 0; s < steps; ++s) {
+      if (s > 0 && s % 16 == 0 && s + 16 < steps) fill(2 * s + 32);  // the half that was used up last
+      unsigned char* stage = stages + (s & 1) * kStageBytes4;
+      copies_wait<1>();  // this lane's pieces of step s have landed ...
+      __syncwarp();      // ... and the other lanes'
+      const int2 entry = *reinterpret_cast<const int2*>(&refs.pos[2 * s % kRefs4]);
       if (p.k_new != nullptr) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          if (entry[i] < 0 || entry[i] / kPage != sp.t / kPage) continue;
+        for (int i = 0; i < 2; ++i) {
+          const int pos = i ? entry.y : entry.x;
+          if (pos < 0 || pos / kPage != sp.t / kPage) continue;
           // commit: the step's K/V, quantised, take slot t in the cache and in this copy
           const uint4 v = *reinterpret_cast<const uint4*>((lane < 16 ? p.k_new : p.v_new) +
                                                           (size_t)bg * kHeadDim + 8 * (lane & 15));
           uint32_t meta;
           const uint32_t word = kv4_quantise(v, lane, meta);
-          const int pb = refs[(s * NP + i) % kRefs4].page;
           kv4_store_row(stage + i * kKv4PageBytes, sp.t % kPage, word, meta, lane);
-          kv4_store_row(p.cache + ((size_t)pb * Hkv + g) * kKv4PageBytes, sp.t % kPage, word, meta, lane);
-          fence_proxy_async_smem();  // this slot is refilled by a bulk copy later
+          kv4_store_row(const_cast<unsigned char*>(refs.src[(2 * s + i) % kRefs4]), sp.t % kPage, word, meta,
+                        lane);
           __syncwarp();
         }
       }
       kv4_step<G, kScores>(stage, entry, sp, qb, kq, qs, st, pw, scores, p.cap, lane);
-      if (lane < NP && s + kStages < my_steps) issue(s + kStages);
-      __syncwarp();
+      issue(s + 2);
     }
-    wcount += my_steps;
+    copies_wait<0>();
 
     // ---- merge the CTA's warps ----
 #pragma unroll
@@ -578,7 +587,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
       st.corr[0] += __shfl_xor_sync(0xffffffffu, st.corr[0], o);
       st.corr[1] += __shfl_xor_sync(0xffffffffu, st.corr[1], o);
     }
-    if (NP == 2) {
+    if (R::kMine == 1) {
       st.l += __shfl_xor_sync(0xffffffffu, st.l, 2);
       st.corr[0] += __shfl_xor_sync(0xffffffffu, st.corr[0], 2);
       st.corr[1] += __shfl_xor_sync(0xffffffffu, st.corr[1], 2);
@@ -591,7 +600,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
         atomicAdd(&s_pages, (unsigned long long)pages_read);
       }
     }
-    __syncthreads();  // every warp is done with its slots: reuse them as merge scratch
+    __syncthreads();  // every warp is done with its stages: reuse them as merge scratch
     if (p.stats != nullptr && tid == 0) {
       if (s_rows) atomicAdd(&p.stats[ODA_STAT_ROWS], s_rows);
       if (s_pages) atomicAdd(&p.stats[ODA_STAT_PAGES], s_pages);
@@ -601,8 +610,8 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     float* Mw = reinterpret_cast<float*>(smem);  // [kW4][HG]
     float* Lw = Mw + kW4 * HG;                   // [kW4][HG]
     float* Aw = Lw + kW4 * HG;                   // [kW4][HG][128]
-    if (gid == 0 && (NP == 1 || tig < 2)) {
-      Mw[warp * HG + R::head(tig)] = st.m == kNoMax ? -INFINITY : st.m;
+    if (gid == 0 && tig < HG) {
+      Mw[warp * HG + R::head(tig)] = st.m == kNoMax && st.l == 0.f ? -INFINITY : st.m;  // (a NaN stays)
       Lw[warp * HG + R::head(tig)] = st.l;
     }
     {
@@ -692,8 +701,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
         if (tid == 0) p.ws_ticket[bg] = 0u;  // leave the workspace zeroed
       }
     }
-    fence_proxy_async_smem();  // merge scratch is the next piece's slot memory
-    __syncthreads();
+    __syncthreads();  // merge scratch is the next piece's stage memory
     x = xe;
   }
 
@@ -787,8 +795,6 @@ int launch_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* 
   p.ws_ticket = reinterpret_cast<unsigned*>(w + wl.ticket_off);
   p.status = kv->dev_status;
   p.stats = kv->stats;
-  p.wait_ns = test_wait_ns();
-  p.test_stall = test_stall() == ODA_STALL_DECODE_RING ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (scores != nullptr) {
     switch (G) {
