@@ -62,11 +62,6 @@ struct Kv4Rows {
   }
 };
 
-__device__ __forceinline__ unsigned cluster_nctas() {
-  unsigned n;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
 __device__ __forceinline__ unsigned dsmem_ld_u32(const unsigned* local, unsigned rank) {
   return __float_as_uint(dsmem_ld(reinterpret_cast<const float*>(local), rank));
 }
@@ -77,13 +72,16 @@ __device__ __forceinline__ unsigned mass_key(float m) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <class Rows>
+constexpr int kKeyCache = 8192;  // keys of a CTA's slots kept in shared memory (more: read again)
+
+template <class Rows, int C>
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams p) {
-  __shared__ unsigned s_hist[2][256];
-  __shared__ unsigned s_bad, s_digit, s_need;
+  __shared__ unsigned s_keys[kKeyCache];
+  __shared__ unsigned s_hist[2][256], s_half[512];
+  __shared__ unsigned s_bad, s_digit, s_need, s_all;
   __shared__ unsigned s_gt[kEvictWarps], s_eq[kEvictWarps], s_total[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const unsigned rank = cluster_ctarank(), C = cluster_nctas();
+  const unsigned rank = C == 1 ? 0u : cluster_ctarank();
   const int bg = blockIdx.x / C;
   const int b = bg / p.hkv, g = bg % p.hkv;
   const int len = p.seq_lens[b];
@@ -92,11 +90,33 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   const int32_t* table = p.block_table + (size_t)b * p.max_blocks;
   const int32_t* dst_table = p.dst_table + (size_t)b * p.dst_blocks;
   const int keep = min(len, p.budget);
+  const float* mass = p.mass + (size_t)bg * p.mass_tokens;
+  float* mass_out = p.mass_out + (size_t)bg * p.mass_tokens;
+  int32_t* kept = p.kept + (size_t)bg * p.budget;
+  const bool usable = !gated && !bad_len;
+  const bool select = usable && len > p.budget;
 
-  // ---- every page that will be read or written must be a page ----
+  // this CTA's slots; which of the sequence's are not kept in any case; how many of those stay
+  const int lo = (int)((long long)len * rank / C), hi = (int)((long long)len * (rank + 1) / C);
+  const int free_lo = p.sink, free_hi = len - p.recent;
+  const int my_lo = max(lo, free_lo), my_hi = min(hi, free_hi);
+  const bool cached = hi - lo <= kKeyCache;
+  auto key = [&](int i) { return cached ? s_keys[i - lo] : mass_key(mass[i]); };
+  // One more of a digit. The keys of a warp share few digits (weights of like size share their
+  // exponents), so equal ones are counted by one of their lanes.
+  auto count = [&](unsigned* hist, bool on, unsigned digit) {
+    const unsigned active = __ballot_sync(0xffffffffu, on);
+    if (on) {
+      const unsigned same = __match_any_sync(active, digit);
+      if ((int)(__ffs(same) - 1) == lane) atomicAdd(&hist[digit], (unsigned)__popc(same));
+    }
+  };
+
+  // ---- before the first cluster barrier: page checks and the first digit's histogram ----
   if (tid == 0) s_bad = 0u;
+  for (int i = tid; i < 512; i += kEvictThreads) s_hist[i >> 8][i & 255] = 0u;
   __syncthreads();
-  if (!gated && !bad_len) {
+  if (usable) {
     const int src_pages = (len + kPage - 1) / kPage, dst_pages = (keep + kPage - 1) / kPage;
     bool bad = false;
     for (int i = rank * kEvictThreads + tid; i < src_pages; i += C * kEvictThreads)
@@ -105,11 +125,23 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       bad |= (unsigned)dst_table[i] >= (unsigned)p.num_blocks;
     if (bad) s_bad = 1u;
   }
+  if (select) {
+    for (int base = my_lo; base < my_hi; base += kEvictThreads) {
+      const int i = base + tid;
+      unsigned k = 0u;
+      if (i < my_hi) {
+        k = mass_key(mass[i]);
+        if (cached) s_keys[i - lo] = k;
+      }
+      count(s_hist[0], i < my_hi, k >> 24);
+    }
+  }
   __syncthreads();
-  cluster_sync();
+  if (C > 1) cluster_sync();
   bool bad_page = false;
-  for (unsigned r = 0; r < C; ++r) bad_page |= dsmem_ld_u32(&s_bad, r) != 0u;
-  const bool skip = gated || bad_len || bad_page;
+#pragma unroll
+  for (int r = 0; r < C; ++r) bad_page |= (C == 1 ? s_bad : dsmem_ld_u32(&s_bad, r)) != 0u;
+  const bool skip = !usable || bad_page;
   // Every CTA of the cluster has read the length: the last of the sequence's KV heads to get
   // here writes the new one (lens_out may be seq_lens).
   if (rank == 0 && tid == 0) {
@@ -121,40 +153,48 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
     }
   }
   if (skip) {
-    cluster_sync();  // nobody leaves while its shared memory may still be read
+    if (C > 1) cluster_sync();  // nobody leaves while its shared memory may still be read
     return;
   }
 
-  const float* mass = p.mass + (size_t)bg * p.mass_tokens;
-  float* mass_out = p.mass_out + (size_t)bg * p.mass_tokens;
-  int32_t* kept = p.kept + (size_t)bg * p.budget;
-
-  if (len > p.budget) {
-    // this CTA's slots, and where the slots that are not kept in any case begin and end
-    const int lo = (int)((long long)len * rank / C), hi = (int)((long long)len * (rank + 1) / C);
-    const int free_lo = p.sink, free_hi = len - p.recent;
-    unsigned need = p.budget - p.sink - p.recent;  // how many of the free slots stay
-    unsigned threshold = 0xffffffffu;              // keys above it stay, `need` of the equal ones
+  if (select) {
+    unsigned need = p.budget - p.sink - p.recent;  // keys above the threshold stay, `need` of its equals
+    unsigned threshold = 0xffffffffu;
     if (need > 0) {
       unsigned prefix = 0u;
 #pragma unroll 1
       for (int pass = 0; pass < 4; ++pass) {
         unsigned* hist = s_hist[pass & 1];
         const int shift = 24 - 8 * pass;
-        for (int i = tid; i < 256; i += kEvictThreads) hist[i] = 0u;
-        __syncthreads();
-        for (int i = max(lo, free_lo) + tid; i < min(hi, free_hi); i += kEvictThreads) {
-          const unsigned k = mass_key(mass[i]);
-          if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+        if (pass > 0) {
+          for (int base = my_lo; base < my_hi; base += kEvictThreads) {
+            const int i = base + tid;
+            const unsigned k = i < my_hi ? key(i) : 0u;
+            count(hist, i < my_hi && (k >> (shift + 8)) == prefix, (k >> shift) & 255u);
+          }
+          __syncthreads();
+          if (C > 1) cluster_sync();
+        }
+        {  // the cluster's histogram: thread (half, digit) sums half the CTAs' counts
+          unsigned n = 0u;
+          const int digit = tid & 255, half = tid >> 8;
+          if constexpr (C == 1) {
+            n = half == 0 ? hist[digit] : 0u;
+          } else {
+            unsigned v[C / 2];
+#pragma unroll
+            for (int r = 0; r < C / 2; ++r) v[r] = dsmem_ld_u32(&hist[digit], half * (C / 2) + r);
+#pragma unroll
+            for (int r = 0; r < C / 2; ++r) n += v[r];
+          }
+          s_half[tid] = n;
         }
         __syncthreads();
-        cluster_sync();
-        if (warp == 0) {  // lane l: digits 8 l .. 8 l + 7, from the top
+        if (warp == 0) {  // lane l: digits 8 l .. 8 l + 7; from the top
           unsigned n[8], sum = 0u;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            n[i] = 0u;
-            for (unsigned r = 0; r < C; ++r) n[i] += dsmem_ld_u32(&hist[8 * lane + i], r);
+            n[i] = s_half[8 * lane + i] + s_half[256 + 8 * lane + i];
             sum += n[i];
           }
           unsigned above = sum;  // keys in this lane's digits and the higher ones
@@ -165,18 +205,39 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
           }
           above -= sum;
           if (above < need && above + sum >= need) {
-            int i = 7;
-            for (; i > 0 && above + n[i] < need; --i) above += n[i];
-            s_digit = 8 * lane + i;
-            s_need = need - above;
+            unsigned a = above, here = 0u;
+            int d = 0;
+            bool found = false;
+#pragma unroll
+            for (int i = 7; i >= 0; --i) {
+              if (!found) {
+                if (a + n[i] >= need) {
+                  found = true;
+                  d = i;
+                  here = n[i];
+                } else {
+                  a += n[i];
+                }
+              }
+            }
+            s_digit = 8 * lane + d;
+            s_need = need - a;
+            s_all = here == need - a;  // every key of the digit stays: no lower digit matters
           }
+        } else if (pass < 3 && tid >= kEvictThreads - 256) {
+          // the other histogram was last read before the cluster barrier above
+          if (pass > 0) s_hist[(pass + 1) & 1][tid - (kEvictThreads - 256)] = 0u;
         }
         __syncthreads();
         prefix = (prefix << 8) | s_digit;
         need = s_need;
-        __syncthreads();
+        if (s_all) {
+          threshold = (prefix << shift) - 1u;  // (not below 0: some free key does not stay)
+          need = 0u;
+          break;
+        }
+        threshold = prefix;
       }
-      threshold = prefix;
     }
 
     // ---- count, then list: warps take consecutive runs of this CTA's slots ----
@@ -188,7 +249,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       if (i < free_lo || i >= free_hi) {
         above = true;
       } else if (p.budget > p.sink + p.recent) {
-        const unsigned k = mass_key(mass[i]);
+        const unsigned k = key(i);
         above = k > threshold;
         equal = k == threshold;
       }
@@ -217,10 +278,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       s_total[1] = eq_before + eq;
     }
     __syncthreads();
-    cluster_sync();
-    for (unsigned r = 0; r < rank; ++r) {
-      gt_before += dsmem_ld_u32(&s_total[0], r);
-      eq_before += dsmem_ld_u32(&s_total[1], r);
+    if (C > 1) cluster_sync();
+#pragma unroll
+    for (int r = 0; r < C - 1; ++r) {
+      const unsigned gr = dsmem_ld_u32(&s_total[0], r), er = dsmem_ld_u32(&s_total[1], r);
+      gt_before += r < (int)rank ? gr : 0u;
+      eq_before += r < (int)rank ? er : 0u;
     }
     for (int base = wlo; base < whi; base += 32) {
       bool a, e;
@@ -237,7 +300,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
     for (int i = rank * kEvictThreads + tid; i < p.budget; i += C * kEvictThreads)
       kept[i] = i < len ? i : -1;
   }
-  cluster_sync();  // the whole list is written
+  if (C > 1) cluster_sync(); else __syncthreads();  // the whole list is written
 
   // ---- move ----
   constexpr int kRowsPerRound = kEvictThreads * kPieces / Rows::kCount;
@@ -255,7 +318,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
       }
     }
     if (tid < rows) m = mass[kept[first + tid]];
-    if (p.in_place) cluster_sync();
+    if (p.in_place) {
+      if (C > 1) cluster_sync(); else __syncthreads();
+    }
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int e = tid + u * kEvictThreads;
@@ -268,7 +333,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   }
   // the slots given up weigh nothing until they are used again
   for (int i = keep + rank * kEvictThreads + tid; i < len; i += C * kEvictThreads) mass_out[i] = 0.f;
-  cluster_sync();  // nobody leaves while its shared memory may still be read
+  if (C > 1) cluster_sync();  // nobody leaves while its shared memory may still be read
 }
 
 // CTAs per cluster: as many (at most 16) as keep all clusters within two waves of one CTA per SM,
@@ -285,7 +350,7 @@ static int prepare_evict(int device, int* most) {
   if (device < 0 || device >= 64) return ODA_ERR_CUDA;
   if (cached[device] == 0) {
     const cudaError_t e =
-        cudaFuncSetAttribute(evict_kernel<Rows>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        cudaFuncSetAttribute(evict_kernel<Rows, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_status(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(16);
@@ -297,7 +362,7 @@ static int prepare_evict(int device, int* most) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, evict_kernel<Rows>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, evict_kernel<Rows, 16>, &cfg) != cudaSuccess) {
       cudaGetLastError();  // not fatal: eight CTAs are portable
       n = 0;
     }
@@ -305,6 +370,21 @@ static int prepare_evict(int device, int* most) {
   }
   *most = cached[device];
   return ODA_OK;
+}
+
+template <class Rows, int C>
+static cudaError_t launch_evict_kernel(const EvictParams& p, long long rows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * C));
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, evict_kernel<Rows, C>, p);
 }
 
 static int evict_args(const oda_kv* kv, const float* mass, int64_t mass_tokens, int sink, int recent,
@@ -369,17 +449,14 @@ static int launch_evict(const oda_kv* kv, const float* mass, int64_t mass_tokens
   const long long rows = (long long)kv->batch * kv->num_kv_heads;
   const int C = evict_cluster(di, rows, (long long)kv->max_blocks_per_seq * kPage, most);
   if (rows * C >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * C));
-  cfg.blockDim = dim3(kEvictThreads);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, evict_kernel<Rows>, p));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (C) {
+    case 1: return cuda_status(launch_evict_kernel<Rows, 1>(p, rows, st));
+    case 2: return cuda_status(launch_evict_kernel<Rows, 2>(p, rows, st));
+    case 4: return cuda_status(launch_evict_kernel<Rows, 4>(p, rows, st));
+    case 8: return cuda_status(launch_evict_kernel<Rows, 8>(p, rows, st));
+    default: return cuda_status(launch_evict_kernel<Rows, 16>(p, rows, st));
+  }
 }
 
 }  // namespace oda

@@ -25,44 +25,82 @@ __device__ __forceinline__ float kv4_min(uint32_t meta) { return bf16hi(meta); }
 // Word of a row that holds dims 8 li .. 8 li + 7 (li < 16).
 __device__ __forceinline__ int kv4_word(int li) { return li < 8 ? 2 * li : 2 * (li - 8) + 1; }
 
+__device__ __forceinline__ uint32_t bf2_max_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Packed fp32 pairs (each lane rounded as the scalar instruction would).
+__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 f2_mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 f2_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // Quantise a row pair, one warp: lane = 16 * isv + li holds dims 8 li .. 8 li + 7 of the K (lanes
 // 0-15) or V row as bf16. Returns the lane's code word; `meta` is its group's word (the same in
 // the group's 8 lanes). m is the group's least value (a bf16 input value, so stored exactly), s
 // the bf16 next at or above (max - m) / 15, so that 15 s spans the group and every value is
 // within s / 2 of what it reads back as. The codes are rint((x - m) / s), division and all
-// roundings as IEEE fp32 has them. A group with an infinity or a NaN, or whose span overflows,
-// reads back as NaN.
+// roundings as IEEE fp32 has them: the product with the reciprocal is within 4e-6 of the quotient, so
+// only a value that close to a half needs the division itself. A group with an infinity or a NaN,
+// or whose span overflows, reads back as NaN.
 __device__ __forceinline__ uint32_t kv4_quantise(const uint4& v, int lane, uint32_t& meta) {
-  float x[8];
-  unpack8(v, x);
-  float lo = x[0], hi = x[0], z = 0.f;
+  // the group's (max, -min) as a bf16 pair, NaN if any value is one
+  constexpr uint32_t kSigns = 0x80008000u;
+  const uint32_t hi = bf2_max_nan(bf2_max_nan(v.x, v.y), bf2_max_nan(v.z, v.w));
+  const uint32_t lo = bf2_max_nan(bf2_max_nan(v.x ^ kSigns, v.y ^ kSigns),
+                                  bf2_max_nan(v.z ^ kSigns, v.w ^ kSigns));
+  uint32_t ends = bf2_max_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    z = fmaf(x[i], 0.f, z);  // NaN as soon as one value is not finite
-  }
-#pragma unroll
-  for (int o = 1; o <= 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  const float span = hi - lo;
-  const unsigned bad = __ballot_sync(0xffffffffu, z != 0.f || isinf(span));
-  if ((bad >> (lane & 24)) & 0xffu) {
-    meta = 0x7fc07fc0u;
-    return 0u;
-  }
+  for (int o = 1; o <= 4; o <<= 1) ends = bf2_max_nan(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+  const float m = -bf16hi(ends), span = bf16lo(ends) - m;
   const uint32_t sbits = (__float_as_uint(__fdiv_rn(span, 15.f)) + 0xffffu) & 0xffff0000u;
+  meta = (sbits >> 16) | __float_as_uint(m);
+  if (!(span <= 3.4028234e38f)) meta = 0x7fc07fc0u;
   const float s = __uint_as_float(sbits);
-  meta = (sbits >> 16) | (__float_as_uint(lo) & 0xffff0000u);
-  uint32_t w = 0;
-  if (s > 0.f) {
+  if (!(s > 0.f) || meta == 0x7fc07fc0u) return 0u;  // a constant group: every code 0
+  const float inv = __frcp_rn(s);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  constexpr float kRound = 12582912.f;  // 1.5 x 2^23: adding it leaves the nearest whole number
+  float2 c[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w |= (uint32_t)min(__float2int_rn(__fdiv_rn(x[i] - lo, s)), 15) << (4 * i);
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = f2_add(make_float2(bf16lo(w[i]), bf16hi(w[i])), make_float2(-m, -m));
+    // (a subnormal scale has no finite reciprocal: neither product's distance is then a number)
+    const float2 t = f2_mul2(a, make_float2(inv, inv));
+    c[i] = f2_add(f2_add(t, make_float2(kRound, kRound)), make_float2(-kRound, -kRound));
+    const float2 d = f2_add(t, make_float2(-c[i].x, -c[i].y));
+    if (!(fmaxf(fabsf(d.x), fabsf(d.y)) < 0.49999f)) {
+      c[i].x = rintf(__fdiv_rn(a.x, s));
+      c[i].y = rintf(__fdiv_rn(a.y, s));
+    }
   }
-  return w;
+  // codes to nibbles: sums of whole numbers below 2^16, then below the exponent of 2^23
+  const float2 k16 = make_float2(256.f, 256.f);
+  const float2 p = f2_fma2(c[1], k16, c[0]), q = f2_fma2(c[3], k16, c[2]);  // c0 + 256 c2, c1 + 256 c3
+  const float x0 = fmaf(p.y, 16.f, p.x) + 8388608.f, x1 = fmaf(q.y, 16.f, q.x) + 8388608.f;
+  return __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x5410);
 }
 
 // Store a quantised row pair (lane layout of kv4_quantise) as token `row` of the page at

@@ -1,15 +1,19 @@
 // Append rows to the 4-bit cache and read rows back ([ODA] 접근 방법: the fully retained history,
 // held in 144 bytes per position and KV head instead of 512).
 //
-// Bound: HBM bytes -- an appended row pair is 512 B read and 144 B written, and a handful of
-// instructions per value. One warp takes one (row, KV head): its lanes hold 16 bytes of the K row
-// (0-15) and of the V row (16-31), so a group of 64 dims is 8 lanes and its range three shuffles.
+// Bound: HBM bytes -- an appended row pair is 512 B read and 144 B written -- and close behind it
+// instruction issue (some 90 instructions a row pair and warp). A warp takes U (row, KV head) units: its
+// first U lanes look up where the units go, all at once, then for each unit the lanes hold 16 bytes of
+// the K row (0-15) and of the V row (16-31), so a group of 64 dims is 8 lanes and its ends three
+// shuffles. U = 8 where there are units enough to fill the GPU with such warps (the chain of dependent
+// loads that finds a slot is then paid once for eight units, and four rows are in flight); else U = 1.
 #include "oda_internal.h"
 #include "oda_kv4.cuh"
 
 namespace oda {
 
 constexpr int kRowWarps = 8;
+constexpr int kManyUnits = 8 * kRowWarps * 8 * 148;  // eight CTAs of U = 8 warps per SM
 
 struct RowsParams {
   unsigned char* cache;
@@ -22,87 +26,154 @@ struct RowsParams {
   int* status;
 };
 
-// Where row i goes: the page of (sequence, KV head 0) and the row inside it. False: the row
-// belongs to no sequence, its sequence is gated off, or it has no valid slot (reported).
-__device__ __forceinline__ bool find_slot(const RowsParams& p, int i, int lane, int* page, int* row) {
+// Where row i of KV head g goes: the page and the row inside it (-1: the row belongs to no sequence, its
+// sequence is gated off, or it has no valid slot, which is reported).
+struct Slot {
+  unsigned char* page;
+  int row;
+};
+__device__ __forceinline__ Slot find_slot(const RowsParams& p, int i, int g) {
+  Slot none;
+  none.page = nullptr;
+  none.row = -1;
   int b = i, before = i, count = 1;
   if (p.cu_rows != nullptr) {
-    b = 0;  // number of sequences that end at or before row i
-    for (int k = lane; k < (p.batch + 31) / 32 * 32; k += 32)
-      b += __popc(__ballot_sync(0xffffffffu, k < p.batch && p.cu_rows[k + 1] <= i));
-    if (b >= p.batch) return false;
+    int lo = 0, hi = p.batch;  // the first sequence that ends after row i
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cu_rows[mid + 1] <= i) lo = mid + 1; else hi = mid;
+    }
+    if (lo >= p.batch) return none;
+    b = lo;
     before = p.cu_rows[b];
     count = p.cu_rows[b + 1] - before;
-    if (i < before || i - before >= count) return false;
+    if (i < before || i - before >= count) return none;
   }
-  if (p.gate != nullptr && p.gate[b] == 0) return false;
+  if (p.gate != nullptr && p.gate[b] == 0) return none;
   const int len = p.seq_lens[b];
   if (len < 1 || len > (long long)p.max_blocks * kPage || count > len) {
-    if (lane == 0) report(p.status, ODA_DEV_BAD_LEN);
-    return false;
+    report(p.status, ODA_DEV_BAD_LEN);
+    return none;
   }
   const int t = len - count + (i - before);
   const int pb = p.block_table[(size_t)b * p.max_blocks + t / kPage];
   if (pb < 0 || pb >= p.num_blocks) {
-    if (lane == 0) report(p.status, ODA_DEV_BAD_BLOCK);
-    return false;
+    report(p.status, ODA_DEV_BAD_BLOCK);
+    return none;
   }
-  *page = pb;
-  *row = t % kPage;
-  return true;
+  Slot s;
+  s.page = p.cache + ((size_t)pb * p.hkv + g) * kKv4PageBytes;
+  s.row = t % kPage;
+  return s;
 }
 
+// The units of this warp: lane l < U finds unit l's row, head and slot, `at` hands them to the warp.
+template <int U>
+struct Units {
+  int i, g;
+  Slot slot;
+  __device__ __forceinline__ Units(const RowsParams& p, int lane) {
+    const long long unit = ((long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * U + (lane < U ? lane : 0);
+    i = (int)(unit / p.hkv);
+    g = (int)(unit % p.hkv);
+    slot.page = nullptr;
+    slot.row = -1;
+    if (lane < U && i < p.num_rows) slot = find_slot(p, i, g);
+  }
+  __device__ __forceinline__ Slot at(int u, int& row_i, int& head) const {
+    row_i = __shfl_sync(0xffffffffu, i, u);
+    head = __shfl_sync(0xffffffffu, g, u);
+    Slot s;
+    s.page = reinterpret_cast<unsigned char*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(slot.page), u));
+    s.row = __shfl_sync(0xffffffffu, slot.row, u);
+    return s;
+  }
+};
+
+constexpr int kInFlight = 4;
+
+template <int U>
 __global__ void __launch_bounds__(kRowWarps * 32)
     kv4_append_kernel(const RowsParams p, const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
                       long long k_stride, long long v_stride) {
+  constexpr int N = U < kInFlight ? U : kInFlight;
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const int i = (int)(unit / p.hkv), g = (int)(unit % p.hkv);
-  if (i >= p.num_rows) return;
-  const int li = lane & 15;
-  const __nv_bfloat16* src = (lane < 16 ? k_new + i * k_stride : v_new + i * v_stride) +
-                             (size_t)g * kHeadDim + 8 * li;
-  const uint4 v = *reinterpret_cast<const uint4*>(src);
-  int pb, row;
-  if (!find_slot(p, i, lane, &pb, &row)) return;
-  uint32_t meta;
-  const uint32_t word = kv4_quantise(v, lane, meta);
-  kv4_store_row(p.cache + ((size_t)pb * p.hkv + g) * kKv4PageBytes, row, word, meta, lane);
+  const Units<U> units(p, lane);
+  const __nv_bfloat16* base = (lane < 16 ? k_new : v_new) + 8 * (lane & 15);
+  const long long stride = lane < 16 ? k_stride : v_stride;
+#pragma unroll
+  for (int u0 = 0; u0 < U; u0 += N) {
+    Slot s[N];
+    uint4 v[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      int i, g;
+      s[n] = units.at(u0 + n, i, g);
+      if (s[n].row >= 0) v[n] = *reinterpret_cast<const uint4*>(base + i * stride + g * kHeadDim);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (s[n].row < 0) continue;  // (uniform)
+      uint32_t meta;
+      const uint32_t word = kv4_quantise(v[n], lane, meta);
+      kv4_store_row(s[n].page, s[n].row, word, meta, lane);
+    }
+  }
 }
 
-template <bool kBf16>
+template <int U, bool kBf16>
 __global__ void __launch_bounds__(kRowWarps * 32)
     kv4_read_kernel(const RowsParams p, void* k_out, void* v_out) {
+  constexpr int N = U < kInFlight ? U : kInFlight;
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const int i = (int)(unit / p.hkv), g = (int)(unit % p.hkv);
-  if (i >= p.num_rows) return;
-  int pb, row;
-  if (!find_slot(p, i, lane, &pb, &row)) return;
   const int li = lane & 15, isv = lane >> 4;
-  const unsigned char* page = p.cache + ((size_t)pb * p.hkv + g) * kKv4PageBytes;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(page + isv * kKv4VOff + row * kKv4RowBytes +
-                                                        4 * kv4_word(li));
-  const uint32_t meta = *reinterpret_cast<const uint32_t*>(page + kKv4MetaOff + row * kKv4MetaBytes +
-                                                           4 * (lane >> 3));
-  const float s = kv4_scale(meta), m = kv4_min(meta);
-  float x[8];
+  const Units<U> units(p, lane);
+  const int code_off = isv * kKv4VOff + 4 * kv4_word(li), meta_off = kKv4MetaOff + 4 * (lane >> 3);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = fmaf((float)((w >> (4 * k)) & 15u), s, m);
-  const size_t at = ((size_t)i * p.hkv + g) * kHeadDim + 8 * li;
-  if constexpr (kBf16) {
-    uint32_t o[4];
+  for (int u0 = 0; u0 < U; u0 += N) {
+    size_t at[N];
+    uint32_t w[N], meta[N];
+    bool ok[N];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-      o[k] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int n = 0; n < N; ++n) {
+      int i, g;
+      const Slot s = units.at(u0 + n, i, g);
+      ok[n] = s.row >= 0;
+      at[n] = ((size_t)i * p.hkv + g) * kHeadDim + 8 * li;
+      if (ok[n]) {
+        w[n] = *reinterpret_cast<const uint32_t*>(s.page + code_off + s.row * kKv4RowBytes);
+        meta[n] = *reinterpret_cast<const uint32_t*>(s.page + meta_off + s.row * kKv4MetaBytes);
+      }
     }
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(isv ? v_out : k_out) + at) =
-        make_uint4(o[0], o[1], o[2], o[3]);
-  } else {
-    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(isv ? v_out : k_out) + at);
-    dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-    dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (!ok[n]) continue;
+      const float2 s = make_float2(kv4_scale(meta[n]), kv4_scale(meta[n]));
+      const float2 m = make_float2(kv4_min(meta[n]), kv4_min(meta[n]));
+      float2 x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // a nibble in the mantissa of 2^23 is 2^23 + c
+        const uint32_t b = w[n] >> (8 * k);
+        const float2 c = make_float2(__uint_as_float(0x4b000000u | (b & 15u)),
+                                     __uint_as_float(0x4b000000u | ((b >> 4) & 15u)));
+        x[k] = f2_fma2(f2_add(c, make_float2(-8388608.f, -8388608.f)), s, m);
+      }
+      if constexpr (kBf16) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[k].x, x[k].y);
+          o[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(isv ? v_out : k_out) + at[n]) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(isv ? v_out : k_out) + at[n]);
+        dst[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        dst[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+      }
+    }
   }
 }
 
@@ -132,7 +203,7 @@ int check_kv4(const oda_kv4* kv) {
 
 // Host checks shared by append and read; *grid is 0 when there is nothing to do.
 static int rows_params(const oda_kv4* kv, int32_t num_rows, const int32_t* cu_rows,
-                       const int32_t* gate, RowsParams* p, unsigned* grid) {
+                       const int32_t* gate, RowsParams* p, unsigned* grid, bool* many) {
   *grid = 0;
   const int rc = check_kv4(kv);
   if (rc != ODA_OK) return rc;
@@ -140,7 +211,9 @@ static int rows_params(const oda_kv4* kv, int32_t num_rows, const int32_t* cu_ro
   if (!aligned_or_null(cu_rows, 4) || !aligned_or_null(gate, 4)) return ODA_ERR_INVALID_ARG;
   if (kv->batch == 0 || num_rows == 0) return ODA_OK;
   const long long units = (long long)num_rows * kv->num_kv_heads;
-  const long long blocks = (units + kRowWarps - 1) / kRowWarps;
+  *many = units >= kManyUnits;
+  const long long per_cta = kRowWarps * (*many ? 8 : 1);
+  const long long blocks = (units + per_cta - 1) / per_cta;
   if (blocks >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
   p->cache = static_cast<unsigned char*>(kv->cache);
   p->block_table = kv->block_table;
@@ -166,7 +239,8 @@ extern "C" int oda_kv4_append(const oda_kv4* kv, const void* k_new, const void* 
                               const int32_t* cu_rows, const int32_t* gate, void* stream) {
   RowsParams p;
   unsigned grid;
-  const int rc = rows_params(kv, num_rows, cu_rows, gate, &p, &grid);
+  bool many = false;
+  const int rc = rows_params(kv, num_rows, cu_rows, gate, &p, &grid, &many);
   if (rc != ODA_OK) return rc;
   const int64_t row = (int64_t)kv->num_kv_heads * kHeadDim;
   if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
@@ -175,7 +249,8 @@ extern "C" int oda_kv4_append(const oda_kv4* kv, const void* k_new, const void* 
   if (k_new == nullptr || v_new == nullptr || !aligned_or_null(k_new, 16) ||
       !aligned_or_null(v_new, 16))
     return ODA_ERR_INVALID_ARG;
-  kv4_append_kernel<<<grid, kRowWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(
+  (many ? kv4_append_kernel<8> : kv4_append_kernel<1>)<<<grid, kRowWarps * 32, 0,
+                                                         static_cast<cudaStream_t>(stream)>>>(
       p, static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new), k_stride,
       v_stride);
   return cuda_status(cudaGetLastError());
@@ -185,7 +260,8 @@ extern "C" int oda_kv4_read(const oda_kv4* kv, void* k_out, void* v_out, int32_t
                             int32_t num_rows, const int32_t* cu_rows, void* stream) {
   RowsParams p;
   unsigned grid;
-  const int rc = rows_params(kv, num_rows, cu_rows, nullptr, &p, &grid);
+  bool many = false;
+  const int rc = rows_params(kv, num_rows, cu_rows, nullptr, &p, &grid, &many);
   if (rc != ODA_OK) return rc;
   if (out_dtype != ODA_F32 && out_dtype != ODA_BF16) return ODA_ERR_INVALID_ARG;
   if (grid == 0) return ODA_OK;
@@ -193,9 +269,8 @@ extern "C" int oda_kv4_read(const oda_kv4* kv, void* k_out, void* v_out, int32_t
       !aligned_or_null(v_out, 16))
     return ODA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (out_dtype == ODA_BF16)
-    kv4_read_kernel<true><<<grid, kRowWarps * 32, 0, st>>>(p, k_out, v_out);
-  else
-    kv4_read_kernel<false><<<grid, kRowWarps * 32, 0, st>>>(p, k_out, v_out);
+  const auto kernel = out_dtype == ODA_BF16 ? (many ? kv4_read_kernel<8, true> : kv4_read_kernel<1, true>)
+                                            : (many ? kv4_read_kernel<8, false> : kv4_read_kernel<1, false>);
+  kernel<<<grid, kRowWarps * 32, 0, st>>>(p, k_out, v_out);
   return cuda_status(cudaGetLastError());
 }

@@ -37,7 +37,7 @@ constexpr int kStages4 = 2;          // steps a warp holds in shared memory: one
 constexpr int kStageBytes4 = kPages4 * kKv4PageBytes;
 constexpr int kRefs4 = 64;           // page references a warp holds (two halves, refilled in turn)
 constexpr int kCtasPerSm4 = 2;
-constexpr int kMinShare4 = 8;        // units per CTA at least (one page per warp)
+constexpr int kMinShare4 = 32;       // pages per CTA at least (two steps a warp)
 constexpr int kPStride = 48;         // words per (page, head) of the weight exchange
 constexpr int kPWords = 2 * 4 * kPStride;
 

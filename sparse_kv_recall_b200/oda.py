@@ -416,101 +416,124 @@ def make_kv4(cache, block_table, seq_lens, dev_status=None, stats=None) -> oda_k
     return kv
 
 
-def _kv_device(kv) -> Optional[int]:
-    """The device of a cache made by make_kv / make_kv4 (None for a handle made by hand)."""
-    refs = getattr(kv, "_refs", None)
-    return refs[0].device.index if refs else None
+# These wrappers run once a layer and step, so their checks are few attribute reads: a tensor's device,
+# type, contiguity and shape, and its address.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 
 
 def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _call(kv, name, stream, args, tensors):
-    """Call an entry point on the cache's device. Every tensor lives there; without a stream
-    argument the work goes to that device's current stream."""
-    dev = _kv_device(kv)
-    for t in tensors:
-        if t is not None and dev is not None and t.device.index != dev:
-            raise ValueError("%s: every tensor must be on the cache's device cuda:%d, got %s"
-                             % (name, dev, t.device))
-    fn = getattr(load(), name)
-    if dev is None or dev == torch.cuda.current_device():
-        _check(fn(ctypes.byref(kv), *args, _stream(stream)), name)
+def _at(t, dev: int, dtype, shape, name):
+    """Address of a contiguous tensor of the given type and shape on device `dev` (None: of None)."""
+    if t is None:
+        return None
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.get_device() != dev:
+        _wrong_device(t, dev, name)
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _wrong_device(t, dev, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    raise ValueError("%s must be on the cache's device cuda:%d, got %s" % (name, dev, t.device))
+
+
+def _kv_device(kv) -> int:
+    """The device of a cache made by make_kv / make_kv4 (the current one for a handle made by hand)."""
+    refs = getattr(kv, "_refs", None)
+    return refs[0].get_device() if refs else (torch.cuda.current_device() if torch.cuda.is_available() else 0)
+
+
+def _call(fn_name, kv, dev, stream, *args):
+    """Call an entry point on device `dev`; without a stream argument the work goes to that device's
+    current stream."""
+    fn = getattr(_lib or load(), fn_name)
+    if stream is not None:
+        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    elif _raw_stream is not None:
+        st = _raw_stream(dev)
+    else:
+        st = torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(kv, *args, st)
     else:
         with torch.cuda.device(dev):
-            _check(fn(ctypes.byref(kv), *args, _stream(stream)), name)
+            rc = fn(kv, *args, st)
+    if rc != ODA_OK:
+        raise OdaError(rc, fn_name)
 
 
-def _row_stride(t, hkv: int, name) -> int:
-    """Element stride of rows [n][hkv][128] whose heads and dims are dense."""
-    if t.dim() != 3 or t.shape[1] != hkv or t.shape[2] != 128:
+def _row_stride(t, hkv: int, dev: int, name) -> int:
+    """Element stride of bf16 rows [n][hkv][128] whose heads and dims are dense."""
+    n, h, d = t.shape if t.dim() == 3 else (0, 0, 0)
+    if h != hkv or d != 128:
         raise ValueError("%s must have shape (rows, %d, 128), got %s" % (name, hkv, tuple(t.shape)))
-    if not t.is_cuda or t.dtype != torch.bfloat16:
-        raise ValueError("%s must be a CUDA bfloat16 tensor" % name)
-    if t.stride(2) != 1 or (hkv > 1 and t.stride(1) != 128):
+    if t.get_device() != dev:
+        _wrong_device(t, dev, name)
+    if t.dtype is not _BF16:
+        raise ValueError("%s must be %s, got %s" % (name, _BF16, t.dtype))
+    s = t.stride()
+    if s[2] != 1 or (hkv > 1 and s[1] != 128):
         raise ValueError("%s: heads and dims must be dense" % name)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), hkv * 128)
+    return s[0] if n > 1 else max(s[0], hkv * 128)
 
 
-def _check_cu_rows(kv, cu_rows, num_rows):
+def _cu_rows(kv, cu_rows, num_rows, dev):
     if cu_rows is None:
         if num_rows != kv.batch:
             raise ValueError("without cu_rows there is one row per sequence: %d rows, batch %d"
                              % (num_rows, kv.batch))
-    else:
-        _shape(cu_rows, (kv.batch + 1,), "cu_rows")
+        return None
+    return _at(cu_rows, dev, _I32, (kv.batch + 1,), "cu_rows")
 
 
 def oda_kv4_append(kv: oda_kv4, k_new, v_new, cu_rows=None, gate=None, stream=None):
     """Quantise bf16 rows [n][Hkv][128] (rows may be strided) into the last slots of their sequences:
     one row per sequence, or rows cu_rows[b] .. cu_rows[b + 1] - 1 (int32 [B + 1]) to sequence b."""
-    ks, vs = _row_stride(k_new, kv.num_kv_heads, "k_new"), _row_stride(v_new, kv.num_kv_heads, "v_new")
+    dev = _kv_device(kv)
+    hkv, n = kv.num_kv_heads, k_new.shape[0]
+    ks, vs = _row_stride(k_new, hkv, dev, "k_new"), _row_stride(v_new, hkv, dev, "v_new")
     _shape(v_new, k_new.shape, "v_new")
-    _check_cu_rows(kv, cu_rows, k_new.shape[0])
-    if gate is not None:
-        _shape(gate, (kv.batch,), "gate")
-    _call(kv, "oda_kv4_append", stream,
-          (k_new.data_ptr(), v_new.data_ptr(), ks, vs, k_new.shape[0],
-           _ptr(cu_rows, torch.int32, "cu_rows"), _ptr(gate, torch.int32, "gate")),
-          (k_new, v_new, cu_rows, gate))
+    _call("oda_kv4_append", kv, dev, stream, k_new.data_ptr(), v_new.data_ptr(), ks, vs, n,
+          _cu_rows(kv, cu_rows, n, dev), _at(gate, dev, _I32, (kv.batch,), "gate"))
 
 
 def oda_kv4_read(kv: oda_kv4, k_out, v_out, cu_rows=None, stream=None):
     """Values of the slots oda_kv4_append would write, into k_out, v_out [n][Hkv][128] (fp32 or bf16)."""
-    _shape(k_out, (k_out.shape[0], kv.num_kv_heads, 128), "k_out")
-    _shape(v_out, k_out.shape, "v_out")
-    if v_out.dtype != k_out.dtype:
+    dev = _kv_device(kv)
+    n = k_out.shape[0]
+    shape = (n, kv.num_kv_heads, 128)
+    if v_out.dtype is not k_out.dtype:
         raise ValueError("k_out and v_out must have one dtype")
-    _check_cu_rows(kv, cu_rows, k_out.shape[0])
-    _call(kv, "oda_kv4_read", stream,
-          (_ptr(k_out, None, "k_out"), _ptr(v_out, None, "v_out"), _out_dtype(k_out), k_out.shape[0],
-           _ptr(cu_rows, torch.int32, "cu_rows")), (k_out, v_out, cu_rows))
+    cu = _cu_rows(kv, cu_rows, n, dev)
+    _call("oda_kv4_read", kv, dev, stream, _at(k_out, dev, None, shape, "k_out"),
+          _at(v_out, dev, None, shape, "v_out"), _out_dtype(k_out), n, cu)
 
 
-def _check_decode(kv, q, out, k_new, v_new, lse):
-    hq = q.shape[1]
-    _shape(q, (kv.batch, hq, 128), "q")
-    _shape(out, (kv.batch, hq, 128), "out")
-    if k_new is not None:
-        _shape(k_new, (kv.batch, kv.num_kv_heads, 128), "k_new")
-    if v_new is not None:
-        _shape(v_new, (kv.batch, kv.num_kv_heads, 128), "v_new")
-    if lse is not None:
-        _shape(lse, (kv.batch, hq), "lse")
-    return hq
+def _decode_args(kv, vis, q, scale, out, k_new, v_new, lse, dev):
+    batch, hq = kv.batch, q.shape[1]
+    row, new = (batch, hq, 128), (batch, kv.num_kv_heads, 128)
+    return (vis, _at(q, dev, _BF16, row, "q"), hq, scale, _at(k_new, dev, _BF16, new, "k_new"),
+            _at(v_new, dev, _BF16, new, "v_new"), _at(out, dev, None, row, "out"), _out_dtype(out),
+            _at(lse, dev, _F32, (batch, hq), "lse"))
 
 
 def oda_kv4_decode(kv: oda_kv4, vis: oda_visibility, q, scale: float, out, ws, k_new=None,
                    v_new=None, lse=None, stream=None):
     """Decode attention over the 4-bit cache under any visibility rule (oda_visibility)."""
-    hq = _check_decode(kv, q, out, k_new, v_new, lse)
-    _call(kv, "oda_kv4_decode", stream,
-          (ctypes.byref(vis), _ptr(q, torch.bfloat16, "q"), hq, scale,
-           _ptr(k_new, torch.bfloat16, "k_new"), _ptr(v_new, torch.bfloat16, "v_new"),
-           _ptr(out, None, "out"), _out_dtype(out), _ptr(lse, torch.float32, "lse"),
-           _ptr(ws, None, "ws"), ws.numel() * ws.element_size()), (q, out, ws, k_new, v_new, lse))
+    dev = _kv_device(kv)
+    _call("oda_kv4_decode", kv, dev, stream, *_decode_args(kv, vis, q, scale, out, k_new, v_new, lse, dev),
+          _at(ws, dev, None, None, "ws"), ws.nbytes)
 
 
 def _size(name, *args) -> int:
@@ -539,17 +562,12 @@ def oda_kv_evict_workspace_size(batch: int) -> int:
 
 
 def _decode_mass(name, kv, vis, q, scale, out, ws, mass_out, mass_in, k_new, v_new, lse, stream):
-    hq = _check_decode(kv, q, out, k_new, v_new, lse)
-    _shape(mass_out, (kv.batch, kv.num_kv_heads, mass_out.shape[2]), "mass_out")
-    if mass_in is not None:
-        _shape(mass_in, mass_out.shape, "mass_in")
-    _call(kv, name, stream,
-          (ctypes.byref(vis), _ptr(q, torch.bfloat16, "q"), hq, scale,
-           _ptr(k_new, torch.bfloat16, "k_new"), _ptr(v_new, torch.bfloat16, "v_new"),
-           _ptr(out, None, "out"), _out_dtype(out), _ptr(lse, torch.float32, "lse"),
-           _ptr(mass_in, torch.float32, "mass_in"), _ptr(mass_out, torch.float32, "mass_out"),
-           mass_out.shape[2], _ptr(ws, None, "ws"), ws.numel() * ws.element_size()),
-          (q, out, ws, k_new, v_new, lse, mass_in, mass_out))
+    dev = _kv_device(kv)
+    shape = (kv.batch, kv.num_kv_heads, mass_out.shape[2])
+    _shape(mass_out, shape, "mass_out")
+    args = _decode_args(kv, vis, q, scale, out, k_new, v_new, lse, dev)
+    _call(name, kv, dev, stream, *args, _at(mass_in, dev, _F32, shape, "mass_in"),
+          _at(mass_out, dev, _F32, None, "mass_out"), shape[2], _at(ws, dev, None, None, "ws"), ws.nbytes)
 
 
 def oda_decode_mass(kv: oda_kv, vis: oda_visibility, q, scale: float, out, ws, mass_out, mass_in=None,
@@ -569,20 +587,14 @@ def oda_kv4_decode_mass(kv: oda_kv4, vis: oda_visibility, q, scale: float, out, 
 
 def _evict(name, kv, mass, sink, recent, budget, dst_block_table, kept, mass_out, seq_lens_out, ws, gate,
            stream):
-    _shape(mass, (kv.batch, kv.num_kv_heads, mass.shape[2]), "mass")
-    _shape(mass_out, mass.shape, "mass_out")
-    _shape(kept, (kv.batch, kv.num_kv_heads, budget), "kept")
-    _shape(dst_block_table, (kv.batch, dst_block_table.shape[1]), "dst_block_table")
-    _shape(seq_lens_out, (kv.batch,), "seq_lens_out")
-    if gate is not None:
-        _shape(gate, (kv.batch,), "gate")
-    _call(kv, name, stream,
-          (_ptr(mass, torch.float32, "mass"), mass.shape[2], sink, recent, budget,
-           _ptr(gate, torch.int32, "gate"), _ptr(dst_block_table, torch.int32, "dst_block_table"),
-           dst_block_table.shape[1], _ptr(kept, torch.int32, "kept"),
-           _ptr(mass_out, torch.float32, "mass_out"), _ptr(seq_lens_out, torch.int32, "seq_lens_out"),
-           _ptr(ws, None, "ws"), ws.numel() * ws.element_size()),
-          (mass, gate, dst_block_table, kept, mass_out, seq_lens_out, ws))
+    dev = _kv_device(kv)
+    batch, hkv = kv.batch, kv.num_kv_heads
+    shape, dst = (batch, hkv, mass.shape[2]), (batch, dst_block_table.shape[1])
+    _shape(kept, (batch, hkv, budget), "kept")
+    _call(name, kv, dev, stream, _at(mass, dev, _F32, shape, "mass"), shape[2], sink, recent, budget,
+          _at(gate, dev, _I32, (batch,), "gate"), _at(dst_block_table, dev, _I32, dst, "dst_block_table"), dst[1],
+          _at(kept, dev, _I32, None, "kept"), _at(mass_out, dev, _F32, shape, "mass_out"),
+          _at(seq_lens_out, dev, _I32, (batch,), "seq_lens_out"), _at(ws, dev, None, None, "ws"), ws.nbytes)
 
 
 def oda_kv_evict(kv: oda_kv, mass, sink: int, recent: int, budget: int, dst_block_table, kept, mass_out,
