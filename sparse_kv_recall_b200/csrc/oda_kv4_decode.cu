@@ -8,7 +8,7 @@
 // pipe (half rate), which unpacks the codes. So both products run on the tensor cores straight from
 // codes, and scales and minima are applied to sums instead of to elements:
 //
-//   K:  s_p = sum_groups [ S_g sum_d (c - 8) q_d + (M_g + 8 S_g) sum_d q_d ]   (S, M of token p)
+//   K:  s_p = sum_groups [ S_g sum_d c q_d + M_g sum_d q_d ]   (S, M of token p)
 //       mma.sync m16n8k16 fp16, A = 16 tokens x codes, B = columns (head, group) that hold the head's q
 //       in the dims of their group and zero elsewhere. q is scaled by a power of two to the top of the
 //       fp16 range: its eight significant bits fit, so every dim within 2^-28 of the head's largest is
@@ -131,8 +131,8 @@ struct Kv4State {
 constexpr float kR0 = 1.2676506e30f;   // 2^100
 constexpr float kNoMax = -1e30f;       // running maximum before any visible score
 
-// The group's q as B fragments and, for the lane's own head, sum q of each group and the factor that
-// undoes q's power of two. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
+// The group's q as B fragments (scaled to q') and, for the lane's own head, sum q' of each group and the
+// factor that undoes q's power of two. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
 // word e = s / 2 of the lane's 16-byte code chunk, which is all group e & 1.
 template <int G>
 __device__ __forceinline__ float load_q4(const __nv_bfloat16* q, int lane, uint32_t (&b)[8][2],
@@ -170,8 +170,8 @@ __device__ __forceinline__ float load_q4(const __nv_bfloat16* q, int lane, uint3
     b[s][1] = mine ? h2_pack(x[e][j + 1] * up, x[e][j + 5] * up) : 0u;
   }
   const int src = 8 * R::head(tig);  // a lane whose column is the lane's head
-  qs[0] = __shfl_sync(0xffffffffu, sum[0], src);
-  qs[1] = __shfl_sync(0xffffffffu, sum[1], src);
+  qs[0] = __shfl_sync(0xffffffffu, sum[0] * up, src);
+  qs[1] = __shfl_sync(0xffffffffu, sum[1] * up, src);
   return __uint_as_float((254u - __shfl_sync(0xffffffffu, f, src)) << 23);
 }
 
@@ -192,7 +192,7 @@ __device__ __forceinline__ int rows_in_page(const SeqPlan& s, int pos) {
 
 // One step over the two pages at `stage` (of a page with a negative entry no scale or minimum is used;
 // its codes are finite numbers whatever they are). kq undoes q's power of two and carries the softmax
-// scale in base 2; qs is sum q times that scale.
+// scale in base 2; qs is sum q' of each group.
 template <int G, bool kScores>
 __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry, const SeqPlan& sp,
                                          const uint32_t (&qb)[8][2], float kq, const float (&qs)[2],
@@ -202,7 +202,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
   const int gid = lane >> 2, tig = lane & 3;
   const int myhead = R::head(tig), mypage = R::page(tig);
 
-  // ---- sums c[page]: token gid groups 0, 1; token gid + 8 groups 0, 1 ----
+  // ---- sums c[page] of c q': token gid groups 0, 1; token gid + 8 groups 0, 1 ----
   float c[2][4];
   const unsigned char* kbase = stage + gid * kKv4RowBytes + 16 * tig;
 #pragma unroll
@@ -210,8 +210,9 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
     const uint4 wa = *reinterpret_cast<const uint4*>(kbase + n * kKv4PageBytes);
     const uint4 wb = *reinterpret_cast<const uint4*>(kbase + n * kKv4PageBytes + 8 * kKv4RowBytes);
     const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
+    // (the codes enter as c - 8; 8 sum q' brings that back, so c is sum c q')
+    c[n][0] = c[n][2] = 8.f * qs[0];
+    c[n][1] = c[n][3] = 8.f * qs[1];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t ca[4], cb[4];
@@ -222,7 +223,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
     }
   }
 
-  // ---- this lane's scores x[page][token gid, gid + 8] and the V meta of those tokens ----
+  // ---- this lane's scores x[page][token gid, gid + 8] (before kq) and the V meta of those tokens ----
   const unsigned char* mbase = stage + mypage * kKv4PageBytes + kKv4MetaOff + gid * kKv4MetaBytes;
   float x[NM][2];
   uint32_t vm[NM][2][2];  // [page][token][group]
@@ -238,8 +239,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
       for (int g = 0; g < 2; ++g) {
         const float cc = (NM == 1 && mypage) ? c[1][2 * i + g] : c[n][2 * i + g];
         const uint32_t km = g ? m.y : m.x;
-        const float s = kv4_scale(km);
-        x[n][i] = fmaf(s * kq, cc, fmaf(fmaf(8.f, s, kv4_min(km)), qs[g], x[n][i]));
+        x[n][i] = fmaf(kv4_scale(km), cc, g ? fmaf(kv4_min(km), qs[g], x[n][i]) : kv4_min(km) * qs[g]);
       }
     }
 
@@ -264,7 +264,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
         float* dst = scores + (size_t)myhead * cap + (mine & ~15) + gid;
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // (what hides a row is looked up again: a score may be -inf)
-          if (whole || (mine >= 0 && row_visible(sp, (mine & ~15) + gid + 8 * i))) dst[8 * i] = x[n][i];
+          if (whole || (mine >= 0 && row_visible(sp, (mine & ~15) + gid + 8 * i))) dst[8 * i] = x[n][i] * kq;
       }
     }
   }
@@ -278,6 +278,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
   };
   float top = fmaxf(x[0][0], x[0][1]);
   if (NM == 2) top = fmaxf(top, fmaxf(x[NM - 1][0], x[NM - 1][1]));
+  top *= kq;
   if (__any_sync(0xffffffffu, top > st.m + kLazyMax)) {
     const float mx = over_head(top);
     const bool up = mx > st.m + kLazyMax;
@@ -299,7 +300,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
   for (int n = 0; n < NM; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float w = ex2_fast(x[n][i] - st.m);
+      const float w = ex2_fast(fmaf(x[n][i], kq, -st.m));
       st.l += w;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -537,9 +538,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
 
     uint32_t qb[8][2];
     float qs[2];
-    float kq = load_q4<G>(p.q + ((size_t)b * p.hq + g * G) * kHeadDim, lane, qb, qs) * p.scale_log2;
-    qs[0] *= p.scale_log2;
-    qs[1] *= p.scale_log2;
+    const float kq = load_q4<G>(p.q + ((size_t)b * p.hq + g * G) * kHeadDim, lane, qb, qs) * p.scale_log2;
     float* scores = nullptr;
     if constexpr (kScores) scores = p.scores + ((size_t)b * p.hq + g * G) * p.cap;
 
