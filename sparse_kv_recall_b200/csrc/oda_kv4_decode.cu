@@ -190,11 +190,19 @@ __device__ __forceinline__ int rows_in_page(const SeqPlan& s, int pos) {
   return max(0, hi - lo + 1) - max(0, ghi - glo + 1);
 }
 
+// What a CTA works on: pages j0 .. j1 - 1 of the list of (sequence b, KV head g), units x .. x_end - 1 of the
+// flattened list; CTAs first .. first + contrib - 1 hold parts of this (b, g). In shared memory, filled in by
+// one thread: every warp's registers are spoken for.
+struct Piece {
+  SeqPlan plan;
+  int b, g, j0, j1, x_end, first, contrib;
+};
+
 // One step over the two pages at `stage` (of a page with a negative entry no scale or minimum is used;
 // its codes are finite numbers whatever they are). kq undoes q's power of two and carries the softmax
 // scale in base 2; qs is sum q' of each group.
 template <int G, bool kScores>
-__device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry, const SeqPlan& sp,
+__device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry, const Piece& piece,
                                          const uint32_t (&qb)[8][2], float kq, const float (&qs)[2],
                                          Kv4State& st, uint32_t* pw, float* scores, int cap, int lane) {
   using R = Roles<G>;
@@ -250,7 +258,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
       const int mine = (NM == 2 ? n : mypage) ? entry.y : entry.x;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (mine < 0 || !row_visible(sp, (mine & ~15) + gid + 8 * i)) {
+        if (mine < 0 || !row_visible(piece.plan, (mine & ~15) + gid + 8 * i)) {
           x[n][i] = -INFINITY;
           vm[n][i][0] = vm[n][i][1] = 0u;
         }
@@ -264,7 +272,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
         float* dst = scores + (size_t)myhead * cap + (mine & ~15) + gid;
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // (what hides a row is looked up again: a score may be -inf)
-          if (whole || (mine >= 0 && row_visible(sp, (mine & ~15) + gid + 8 * i))) dst[8 * i] = x[n][i] * kq;
+          if (whole || (mine >= 0 && row_visible(piece.plan, (mine & ~15) + gid + 8 * i))) dst[8 * i] = x[n][i] * kq;
       }
     }
   }
@@ -417,13 +425,66 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// One warp: references of its pages n0 .. n0 + 31 (page n is entry n % 2 of pair n / 2; a CTA's pairs are
+// strided over its warps). Returns this lane's visible rows + 256 x pages.
+__device__ __forceinline__ int kv4_refs(const Kv4Params& p, const Piece& piece, PageRefs& refs, int n0, int warp,
+                                        int lane) {
+  const int n = n0 + lane;
+  const int j = piece.j0 + ((n >> 1) * kW4 + warp) * 2 + (n & 1);
+  int pos = -1, seen = 0;
+  const unsigned char* src = p.cache;
+  if (j < piece.j1) {
+    const PageRef r = page_ref(p.plan, piece.plan, piece.b, j);
+    if (r.err != 0) {
+      report(p.status, r.err);
+    } else {
+      const int rows = rows_in_page(piece.plan, r.lp * kPage);
+      if (rows > 0) pos = r.lp * kPage + rows - 1;
+      src = p.cache + ((size_t)r.pb * p.hkv + piece.g) * kKv4PageBytes;
+      seen = rows + 256;
+    }
+  }
+  refs.pos[n % kRefs4] = pos;
+  refs.src[n % kRefs4] = src;
+  return seen;
+}
+
+// What a step needs rarely is called, not inlined: it keeps the step's registers and code to itself (ragged
+// 8K..64K batch: 153.5 us with both inlined, 148.6 so).
+__device__ __noinline__ int kv4_refs_call(const Kv4Params& p, const Piece& piece, PageRefs& refs, int n0, int warp,
+                                          int lane) {
+  return kv4_refs(p, piece, refs, n0, warp, lane);
+}
+
+// One warp: if the step holds the page of slot t, the step's K/V, quantised, take the slot in the cache
+// and in this copy.
+__device__ __noinline__ void kv4_commit(const Kv4Params& p, const Piece& piece, const PageRefs& refs, int s,
+                                        unsigned char* stage, int lane) {
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const int pos = refs.pos[(2 * s + i) % kRefs4];
+    if (pos < 0 || pos / kPage != piece.plan.t / kPage) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>((lane < 16 ? p.k_new : p.v_new) +
+                                                    ((size_t)piece.b * p.hkv + piece.g) * kHeadDim +
+                                                    8 * (lane & 15));
+    uint32_t meta;
+    const uint32_t word = kv4_quantise(v, lane, meta);
+    const int row = piece.plan.t % kPage;
+    kv4_store_row(stage + i * kKv4PageBytes, row, word, meta, lane);
+    kv4_store_row(const_cast<unsigned char*>(refs.src[(2 * s + i) % kRefs4]), row, word, meta, lane);
+  }
+  __syncwarp();
+}
+
 template <int G, bool kScores>
-__global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(const Kv4Params p) {
+__global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
+    kv4_decode_kernel(const __grid_constant__ Kv4Params p) {
   using R = Roles<G>;
   constexpr int HG = R::kHeads;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int s_align, s_last;
   __shared__ unsigned long long s_rows, s_pages;
+  __shared__ Piece piece;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   unsigned char* stages = smem + warp * kStages4 * kStageBytes4;
@@ -431,14 +492,15 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
   PageRefs& refs = reinterpret_cast<PageRefs*>(smem + Kv4Smem::kRefOff)[warp];
   int* pre = reinterpret_cast<int*>(smem + Kv4Smem::kPreOff);
   const int B = p.batch, Hkv = p.hkv;
-  const int P = gridDim.x, cta = blockIdx.x;
+  const int cta = blockIdx.x;
 
-  // ---- prefix of visible units per sequence, share alignment ----
+  // ---- prefix of visible units per sequence, shares, this CTA's first piece ----
   if (tid == 0) {
     s_rows = 0;
     s_pages = 0;
     pre[0] = 0;
   }
+#pragma unroll 1
   for (int b = tid; b < B; b += kThreads4) {
     const SeqPlan sp = make_plan(p.plan, b);
     pre[b + 1] = sp.npages * Hkv;
@@ -448,6 +510,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
   if (warp == 0) {
     int carry = 0;
     unsigned vmin = 0xffffffffu, vmax = 0u, active = 0u;
+#pragma unroll 1
     for (int base = 0; base < B; base += 32) {
       const int i = base + lane;
       int v = i < B ? pre[i + 1] : 0;
@@ -467,60 +530,54 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
     if (lane == 0) s_align = (active > 0 && vmin == vmax) ? (int)active * Hkv : 0;
   }
   __syncthreads();
-  const long long T = pre[B];
   if constexpr (kScores) griddep_launch_dependents();
 
   // Equal contiguous shares; with equal page counts the CTA count is a multiple of the non-empty
   // (sequence, KV head) pairs, so that every share falls inside one of them.
-  int Pe = (int)min((long long)P, (T + kMinShare4 - 1) / kMinShare4);
+  const int T = pre[B];
+  int Pe = T > 0 ? min((int)gridDim.x, (T - 1) / kMinShare4 + 1) : 0;
   if (s_align > 0) {
     const int up = (Pe + s_align - 1) / s_align * s_align;
-    if (up <= P) Pe = up;
+    if (up <= (int)gridDim.x) Pe = up;
     else if (Pe >= s_align) Pe -= Pe % s_align;
   }
+  // CTA c's share is [c T / Pe, (c + 1) T / Pe)
+  const int each = Pe > 0 ? T / Pe : 0, more = Pe > 0 ? T % Pe : 0;
+  const int share_end = cta < Pe ? (cta + 1) * each + (cta + 1) * more / Pe : 0;
+  int x = cta < Pe ? cta * each + cta * more / Pe : 0;
   const uint64_t policy = l2_evict_first_policy();
-  long long x = cta < Pe ? (T * cta) / Pe : 0;
-  const long long x_end = cta < Pe ? (T * (cta + 1)) / Pe : 0;
-  while (x < x_end) {
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= x) lo = mid; else hi = mid - 1;
-    }
-    const int b = lo;
-    const int npg = (pre[b + 1] - pre[b]) / Hkv;
-    const long long off = x - pre[b];
-    const int g = (int)(off / npg);
-    const int j0 = (int)(off - (long long)g * npg);
-    const long long seg0 = pre[b] + (long long)g * npg, seg1 = seg0 + npg;
-    const long long xe = min(x_end, seg1);
-    const int j1 = j0 + (int)(xe - x);
-    const SeqPlan sp = make_plan(p.plan, b);
-    const int bg = b * Hkv + g;
 
-    // this warp's steps: pairs of consecutive list entries, strided over the warps
-    const int pairs = (j1 - j0 + 1) / 2;
+  // (Whatever a piece or a CTA does once is written at one place in these loops: at several, inlined, it made
+  // the kernel 108 KB of code, much of whose first execution waited for the instruction cache.)
+#pragma unroll 1
+  while (x < share_end) {
+    if (tid == 0) {
+      int lo = 0, hi = B - 1;  // the last sequence that starts at or before unit x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= x) lo = mid; else hi = mid - 1;
+      }
+      const int npg = (pre[lo + 1] - pre[lo]) / Hkv;
+      piece.plan = make_plan(p.plan, lo);
+      piece.b = lo;
+      piece.g = (x - pre[lo]) / npg;
+      const int seg0 = pre[lo] + piece.g * npg;
+      piece.j0 = x - seg0;
+      piece.x_end = min(share_end, seg0 + npg);
+      piece.j1 = piece.j0 + (piece.x_end - x);
+      piece.first = cta_of(seg0, T, Pe);
+      piece.contrib = cta_of(seg0 + npg - 1, T, Pe) - piece.first + 1;
+    }
+    __syncthreads();
+    const int b = piece.b, g = piece.g, bg = b * Hkv + g;
+    const int pairs = (piece.j1 - piece.j0 + 1) / 2;  // of pages, strided over the warps
     const int steps = pairs > warp ? (pairs - warp + kW4 - 1) / kW4 : 0;
     unsigned rows_vis = 0, pages_read = 0;  // this lane's pages
-    auto fill = [&](int n0) {  // references of pages n0 .. n0 + 31; page n is entry n % 2 of step n / 2
-      const int n = n0 + lane;
-      const int j = j0 + ((n >> 1) * kW4 + warp) * 2 + (n & 1);
-      int pos = -1;
-      const unsigned char* src = p.cache;
-      if ((n >> 1) < steps && j < j1) {
-        const PageRef r = page_ref(p.plan, sp, b, j);
-        if (r.err != 0) {
-          report(p.status, r.err);
-        } else {
-          const int rows = rows_in_page(sp, r.lp * kPage);
-          if (rows > 0) pos = r.lp * kPage + rows - 1;
-          src = p.cache + ((size_t)r.pb * Hkv + g) * kKv4PageBytes;
-          rows_vis += rows;
-          ++pages_read;
-        }
-      }
-      refs.pos[n % kRefs4] = pos;
-      refs.src[n % kRefs4] = src;
+
+    auto fill = [&](int n0) {
+      const int seen = kv4_refs(p, piece, refs, n0, warp, lane);
+      rows_vis += seen & 255;
+      pages_read += seen >> 8;
     };
     auto issue = [&](int s) {  // one group of copies a step, empty past the last
       if (s < steps) {
@@ -530,11 +587,12 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
       }
       copies_commit();
     };
-    fill(0);
-    if (steps > 16) fill(32);
-    __syncwarp();
-    issue(0);
-    issue(1);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {  // step 0 on its way before the other half of the references is looked up
+      if (h == 0 || steps > 16) fill(32 * h);
+      __syncwarp();
+      issue(h);
+    }
 
     uint32_t qb[8][2];
     float qs[2];
@@ -552,29 +610,19 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.acc[t][i] = 0.f;
 
+#pragma unroll 1
     for (int s = 0; s < steps; ++s) {
-      if (s > 0 && s % 16 == 0 && s + 16 < steps) fill(2 * s + 32);  // the half that was used up last
+      if (s > 0 && s % 16 == 0 && s + 16 < steps) {  // the half that was used up last
+        const int seen = kv4_refs_call(p, piece, refs, 2 * s + 32, warp, lane);
+        rows_vis += seen & 255;
+        pages_read += seen >> 8;
+      }
       unsigned char* stage = stages + (s & 1) * kStageBytes4;
       copies_wait<1>();  // this lane's pieces of step s have landed ...
       __syncwarp();      // ... and the other lanes'
       const int2 entry = *reinterpret_cast<const int2*>(&refs.pos[2 * s % kRefs4]);
-      if (p.k_new != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int pos = i ? entry.y : entry.x;
-          if (pos < 0 || pos / kPage != sp.t / kPage) continue;
-          // commit: the step's K/V, quantised, take slot t in the cache and in this copy
-          const uint4 v = *reinterpret_cast<const uint4*>((lane < 16 ? p.k_new : p.v_new) +
-                                                          (size_t)bg * kHeadDim + 8 * (lane & 15));
-          uint32_t meta;
-          const uint32_t word = kv4_quantise(v, lane, meta);
-          kv4_store_row(stage + i * kKv4PageBytes, sp.t % kPage, word, meta, lane);
-          kv4_store_row(const_cast<unsigned char*>(refs.src[(2 * s + i) % kRefs4]), sp.t % kPage, word, meta,
-                        lane);
-          __syncwarp();
-        }
-      }
-      kv4_step<G, kScores>(stage, entry, sp, qb, kq, qs, st, pw, scores, p.cap, lane);
+      if (p.k_new != nullptr) kv4_commit(p, piece, refs, s, stage, lane);
+      kv4_step<G, kScores>(stage, entry, piece, qb, kq, qs, st, pw, scores, p.cap, lane);
       issue(s + 2);
     }
     copies_wait<0>();
@@ -631,9 +679,9 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
       }
     }
     __syncthreads();
-    const int c_first = cta_of(seg0, T, Pe);
-    const int n_contrib = cta_of(seg1 - 1, T, Pe) - c_first + 1;
+    const int n_contrib = piece.contrib;
     const size_t slot = (size_t)cta + bg;
+#pragma unroll 1
     for (int e = tid; e < G * kHeadDim; e += kThreads4) {
       const int h = e / kHeadDim, dim = e % kHeadDim;
       float M = -INFINITY;
@@ -664,16 +712,30 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
       if (tid == 0) s_last = ticket_arrive(&p.ws_ticket[bg]) == (unsigned)(n_contrib - 1);
       __syncthreads();  // ... and the last CTA's thread 0 acquired everyone's partials
       if (s_last) {
-        const size_t s0 = (size_t)c_first + bg;
-        float* sw = reinterpret_cast<float*>(smem);  // [n_contrib][G] log-sums, then weights
+        // The partials come into shared memory by asynchronous copies, as many at a time as the stages
+        // hold (all of a short call's at once), the first ones beside the log-sums.
+        const size_t s0 = (size_t)piece.first + bg;
+        float* sw = reinterpret_cast<float*>(smem);      // [n_contrib][G] log-sums, then weights
+        float* so = sw + (n_contrib * G + 3) / 4 * 4;    // [chunk][G][128]
+        const int chunk = (kW4 * kStages4 * kStageBytes4 / 4 - (n_contrib * G + 3)) / (G * kHeadDim);
+        auto bring = [&](int first) {
+          const int n = min(chunk, n_contrib - first) * G * kHeadDim / 4;
+          const float* src = p.ws_o + (s0 + first) * G * kHeadDim;
+#pragma unroll 4
+          for (int i = tid; i < n; i += kThreads4) cp_async16(so + 4 * i, src + 4 * i);
+        };
+        bring(0);
+#pragma unroll 1
         for (int i = tid; i < n_contrib * G; i += kThreads4) sw[i] = __ldcg(&p.ws_lse[s0 * G + i]);
         __shared__ float s_max[4], s_sum[4];
         __syncthreads();
         if (warp < G) {
           float m = -INFINITY, sum = 0.f;
+#pragma unroll 1
           for (int s = lane; s < n_contrib; s += 32) m = fmaxf(m, sw[s * G + warp]);
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll 1
           for (int s = lane; s < n_contrib; s += 32) {
             const float ls = sw[s * G + warp];
             const float w = ls == -INFINITY ? 0.f : ex2_fast(ls - m);
@@ -687,27 +749,47 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4) kv4_decode_kernel(cons
             s_sum[warp] = sum;
           }
         }
-        __syncthreads();
-        for (int e = tid; e < G * kHeadDim; e += kThreads4) {
-          const int h = e / kHeadDim, dim = e % kHeadDim;
-          float a = 0.f;
-          for (int s = 0; s < n_contrib; ++s)
-            a = fmaf(sw[s * G + h], __ldcg(&p.ws_o[((s0 + s) * G + h) * kHeadDim + dim]), a);
-          const float M = s_max[h], L = s_sum[h];
-          const bool none = M == -INFINITY;
-          kv4_write(p, b, g * G + h, dim, none ? 0.f : a / L, none ? -INFINITY : M + log2f(L));
+        constexpr int kMine = (G * kHeadDim + kThreads4 - 1) / kThreads4;
+        float a[kMine] = {};
+#pragma unroll 1
+        for (int first = 0; first < n_contrib; first += chunk) {
+          if (first > 0) {
+            __syncthreads();  // everyone is done with the chunk before
+            bring(first);
+          }
+          cp_async_wait_all();
+          __syncthreads();
+          const int n = min(chunk, n_contrib - first);
+#pragma unroll
+          for (int k = 0; k < kMine; ++k) {
+            const int e = tid + k * kThreads4;
+            if (e < G * kHeadDim)
+#pragma unroll 4
+              for (int s = 0; s < n; ++s)
+                a[k] = fmaf(sw[(first + s) * G + e / kHeadDim], so[s * G * kHeadDim + e], a[k]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+          const int e = tid + k * kThreads4, h = e / kHeadDim;
+          if (e >= G * kHeadDim) break;
+          const bool none = s_max[h] == -INFINITY;
+          kv4_write(p, b, g * G + h, e % kHeadDim, none ? 0.f : a[k] / s_sum[h],
+                    none ? -INFINITY : s_max[h] + log2f(s_sum[h]));
         }
         if (tid == 0) p.ws_ticket[bg] = 0u;  // leave the workspace zeroed
       }
     }
-    __syncthreads();  // merge scratch is the next piece's stage memory
-    x = xe;
+    x = piece.x_end;
+    __syncthreads();  // merge scratch is the next piece's stage memory, `piece` the next piece
   }
 
   // Sequences with nothing visible (bad length, empty keep list) but not gated off.
-  for (int i = cta; i < B * Hkv; i += P) {
+#pragma unroll 1
+  for (int i = cta; i < B * Hkv; i += gridDim.x) {
     const int b = i / Hkv;
     if (pre[b + 1] == pre[b] && !(p.plan.gate != nullptr && p.plan.gate[b] == 0))
+#pragma unroll 1
       for (int e = tid; e < G * kHeadDim; e += kThreads4)
         kv4_write(p, b, (i % Hkv) * G + e / kHeadDim, e % kHeadDim, 0.f, -INFINITY);
   }
