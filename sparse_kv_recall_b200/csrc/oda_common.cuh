@@ -319,6 +319,24 @@ inline int cuda_status(cudaError_t e) {
   return ODA_ERR_CUDA;
 }
 
+// Launch with a programmatic dependency on the kernel before it in the stream: the grid may be set up
+// while that one finishes. The kernel calls griddep_wait() before it touches anything.
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                                    cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- host side: per-device launch facts --------------------------------------------------
 struct DeviceInfo {
   int device = -1;

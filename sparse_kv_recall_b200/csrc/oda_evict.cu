@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   __shared__ unsigned s_gt[kEvictWarps], s_eq[kEvictWarps], s_total[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned rank = C == 1 ? 0u : cluster_ctarank();
+  griddep_launch_dependents();
+  griddep_wait();
   const int bg = blockIdx.x / C;
   const int b = bg / p.hkv, g = bg % p.hkv;
   const int len = p.seq_lens[b];
@@ -378,12 +380,14 @@ static cudaError_t launch_evict_kernel(const EvictParams& p, long long rows, cud
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(kEvictThreads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = C > 1 ? 1 : 0;
+  cfg.numAttrs = C > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, evict_kernel<Rows, C>, p);
 }
 

@@ -98,6 +98,8 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     kv4_append_kernel(const RowsParams p, const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
                       long long k_stride, long long v_stride) {
   constexpr int N = U < kInFlight ? U : kInFlight;
+  griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31;
   const Units<U> units(p, lane);
   const __nv_bfloat16* base = (lane < 16 ? k_new : v_new) + 8 * (lane & 15);
@@ -126,6 +128,8 @@ template <int U, bool kBf16>
 __global__ void __launch_bounds__(kRowWarps * 32)
     kv4_read_kernel(const RowsParams p, void* k_out, void* v_out) {
   constexpr int N = U < kInFlight ? U : kInFlight;
+  griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31;
   const int li = lane & 15, isv = lane >> 4;
   const Units<U> units(p, lane);
@@ -249,11 +253,10 @@ extern "C" int oda_kv4_append(const oda_kv4* kv, const void* k_new, const void* 
   if (k_new == nullptr || v_new == nullptr || !aligned_or_null(k_new, 16) ||
       !aligned_or_null(v_new, 16))
     return ODA_ERR_INVALID_ARG;
-  (many ? kv4_append_kernel<8> : kv4_append_kernel<1>)<<<grid, kRowWarps * 32, 0,
-                                                         static_cast<cudaStream_t>(stream)>>>(
-      p, static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new), k_stride,
-      v_stride);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_dependent(
+      many ? kv4_append_kernel<8> : kv4_append_kernel<1>, grid, kRowWarps * 32, 0,
+      static_cast<cudaStream_t>(stream), p, static_cast<const __nv_bfloat16*>(k_new),
+      static_cast<const __nv_bfloat16*>(v_new), (long long)k_stride, (long long)v_stride));
 }
 
 extern "C" int oda_kv4_read(const oda_kv4* kv, void* k_out, void* v_out, int32_t out_dtype,
@@ -271,6 +274,5 @@ extern "C" int oda_kv4_read(const oda_kv4* kv, void* k_out, void* v_out, int32_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto kernel = out_dtype == ODA_BF16 ? (many ? kv4_read_kernel<8, true> : kv4_read_kernel<1, true>)
                                             : (many ? kv4_read_kernel<8, false> : kv4_read_kernel<1, false>);
-  kernel<<<grid, kRowWarps * 32, 0, st>>>(p, k_out, v_out);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_dependent(kernel, grid, kRowWarps * 32, 0, st, p, k_out, v_out));
 }

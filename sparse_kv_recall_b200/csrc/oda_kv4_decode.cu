@@ -494,6 +494,8 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
   const int B = p.batch, Hkv = p.hkv;
   const int cta = blockIdx.x;
 
+  griddep_launch_dependents();
+  griddep_wait();
   // ---- prefix of visible units per sequence, shares, this CTA's first piece ----
   if (tid == 0) {
     s_rows = 0;
@@ -530,7 +532,6 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
     if (lane == 0) s_align = (active > 0 && vmin == vmax) ? (int)active * Hkv : 0;
   }
   __syncthreads();
-  if constexpr (kScores) griddep_launch_dependents();
 
   // Equal contiguous shares; with equal page counts the CTA count is a multiple of the non-empty
   // (sequence, KV head) pairs, so that every share falls inside one of them.
@@ -834,8 +835,8 @@ static int launch_kv4(const Kv4Params& p, const DeviceInfo& di, cudaStream_t st)
     if (e != cudaSuccess) return cuda_status(e);
     done[di.device] = true;
   }
-  kv4_decode_kernel<G, kScores><<<di.sms * kCtasPerSm4, kThreads4, Kv4Smem::kBytes, st>>>(p);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_dependent(kv4_decode_kernel<G, kScores>, di.sms * kCtasPerSm4, kThreads4,
+                                      Kv4Smem::kBytes, st, p));
 }
 
 int launch_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q, int hq,

@@ -50,6 +50,7 @@ __device__ __forceinline__ bool page_listed(const PlanArgs& a, const SeqPlan& s,
 // touched; otherwise every position of the sequence is written.
 template <bool kAlias>
 __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassParams p) {
+  griddep_launch_dependents();
   griddep_wait();
   const int bg = blockIdx.x / p.blocks_per_row;
   const int b = bg / p.hkv, g = bg % p.hkv;
@@ -167,17 +168,9 @@ static int decode_mass(const oda_kv* kv, const oda_kv4* kv4, const oda_visibilit
   p.mass_out = mass_out;
   p.mass_tokens = mass_tokens;
   p.blocks_per_row = (int)blocks_per_row;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks_per_row * kv->batch * kv->num_kv_heads));
-  cfg.blockDim = dim3(kMassThreads);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_status(mass_out == mass_in ? cudaLaunchKernelEx(&cfg, mass_kernel<true>, p)
-                                         : cudaLaunchKernelEx(&cfg, mass_kernel<false>, p));
+  return cuda_status(launch_dependent(mass_out == mass_in ? mass_kernel<true> : mass_kernel<false>,
+                                      (unsigned)(blocks_per_row * kv->batch * kv->num_kv_heads), kMassThreads, 0,
+                                      static_cast<cudaStream_t>(stream), p));
 }
 
 }  // namespace oda
