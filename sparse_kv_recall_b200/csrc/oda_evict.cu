@@ -3,12 +3,17 @@
 // slot order (the Local rule takes "recent" from the slot order), and move to the destination pages,
 // which may be the source's own.
 //
-// One thread-block cluster takes one (sequence, KV head); its CTAs share the slots. The threshold
-// weight is found by a radix select over order-preserving 32-bit keys, eight bits a pass, the
-// histograms summed through distributed shared memory; every later decision follows from it and
-// from counts, so the result does not depend on any order of execution. Bound: memory -- a kept
-// row is read and written once (512 bytes in bf16, 144 in 4 bits), a weight is read a few times,
-// mostly out of L2.
+// (A launch runs most of this code once, so loops of few trips are not unrolled: the instruction cache is cold.)
+//
+// One thread-block cluster takes one (sequence, KV head). The threshold weight is found by a radix select
+// over order-preserving 32-bit keys, eight bits a pass from the highest bit in which any two keys differ;
+// every later decision follows from it and from
+// counts, so the result does not depend on any order of execution. Up to kAlone slots every CTA of the
+// cluster selects by itself, from all the keys, and moves its share of the rows: a pass is then two CTA
+// barriers, where histograms summed through distributed shared memory cost a cluster barrier and a remote
+// read (2304 slots, budget 2048, one sequence of 8 KV heads: 22.9 us with shared histograms, 13.0 so). Longer sequences are shared out over the cluster. Bound: memory -- a kept row is
+// read and written once (512 bytes in bf16, 144 in 4 bits), a weight is read a few times, mostly out of
+// L2 or shared memory.
 //
 // In place, a move must not overwrite a row that has not been read. The i-th kept slot p_i is >= i,
 // so when the rows of a round, a run [i0, i1) of the kept list, are all in registers before the
@@ -40,25 +45,28 @@ struct EvictParams {
   int dst_blocks;
   int32_t* kept;
   int32_t* lens_out;
-  unsigned* ticket;   // [batch]
+  unsigned* ticket;   // [batch], used with lens_alias
   int in_place;       // the destination may be the source: order loads before stores
+  int lens_alias;     // lens_out is seq_lens
   int* status;
 };
 
-// 16-byte pieces of a row pair, and where piece i of (page, KV head, row) lies.
+// 16-byte pieces of a row pair, and where piece i of KV head g's row `at` (page * 16 + row in it) lies.
 struct Bf16Rows {
   static constexpr int kCount = 32;
-  __device__ static unsigned char* at(const EvictParams& p, int pb, int g, int row, int i) {
-    const size_t off = (((size_t)pb * p.hkv + g) * kPage + row) * kRowBytes;
+  __device__ static unsigned char* at(const EvictParams& p, unsigned at, int g, int i) {
+    const size_t off = (((size_t)(at / kPage) * p.hkv + g) * kPage + at % kPage) * kRowBytes;
     return (i < 16 ? p.k_cache : p.v_cache) + off + 16 * (i & 15);
   }
 };
 struct Kv4Rows {
   static constexpr int kCount = 9;
-  __device__ static unsigned char* at(const EvictParams& p, int pb, int g, int row, int i) {
-    unsigned char* page = p.k_cache + ((size_t)pb * p.hkv + g) * kKv4PageBytes;
-    if (i == 8) return page + kKv4MetaOff + row * kKv4MetaBytes;
-    return page + (i >> 2) * kKv4VOff + row * kKv4RowBytes + 16 * (i & 3);
+  __device__ static unsigned char* at(const EvictParams& p, unsigned at, int g, int i) {
+    const unsigned row = at % kPage;
+    unsigned char* page = p.k_cache + ((size_t)(at / kPage) * p.hkv + g) * kKv4PageBytes;
+    const unsigned off = i == 8 ? kKv4MetaOff + row * kKv4MetaBytes
+                                : (i >> 2) * kKv4VOff + row * kKv4RowBytes + 16 * (i & 3);
+    return page + off;
   }
 };
 
@@ -72,14 +80,44 @@ __device__ __forceinline__ unsigned mass_key(float m) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kKeyCache = 8192;  // keys of a CTA's slots kept in shared memory (more: read again)
+// The least of every lane's lo and the greatest of every lane's hi.
+__device__ __forceinline__ void warp_range(unsigned& lo, unsigned& hi) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+}
+
+__device__ __forceinline__ unsigned warp_scan(unsigned v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+constexpr int kKeyCache = 8192;    // keys held in shared memory: all of a sequence's up to as many slots
+constexpr int kAlone = kKeyCache;  // (each CTA then selects by itself), else a CTA's share (more: read again)
+
+constexpr int kFew = 128;
+
+struct EvictSmem {
+  unsigned keys[kKeyCache];
+  uint16_t list[kAlone];      // alone: the kept slots
+  unsigned hist[2][256];
+  unsigned bad, digit, need, here, kmin, kmax, threshold;
+  unsigned few[kFew], nfew;   // keys of the digit that holds the threshold, once they are few
+  unsigned wmin[kEvictWarps], wmax[kEvictWarps];
+  unsigned gt[kEvictWarps], eq[kEvictWarps], total[2];
+  unsigned src[2][kEvictThreads], dst[2][kEvictThreads];  // rows of two rounds, as page * 16 + row
+};
 
 template <class Rows, int C>
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams p) {
-  __shared__ unsigned s_keys[kKeyCache];
-  __shared__ unsigned s_hist[2][256], s_half[512];
-  __shared__ unsigned s_bad, s_digit, s_need, s_all;
-  __shared__ unsigned s_gt[kEvictWarps], s_eq[kEvictWarps], s_total[2];
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  EvictSmem& s = *reinterpret_cast<EvictSmem*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned rank = C == 1 ? 0u : cluster_ctarank();
   griddep_launch_dependents();
@@ -97,245 +135,323 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictParams 
   int32_t* kept = p.kept + (size_t)bg * p.budget;
   const bool usable = !gated && !bad_len;
   const bool select = usable && len > p.budget;
+  const bool alone = C == 1 || len <= kAlone;  // (uniform over the cluster)
+  const int parts = alone ? 1 : C, part = alone ? 0 : (int)rank;
 
-  // this CTA's slots; which of the sequence's are not kept in any case; how many of those stay
-  const int lo = (int)((long long)len * rank / C), hi = (int)((long long)len * (rank + 1) / C);
+  // the slots this CTA selects from; which are not kept in any case
+  const int lo = (int)((long long)len * part / parts), hi = (int)((long long)len * (part + 1) / parts);
   const int free_lo = p.sink, free_hi = len - p.recent;
   const int my_lo = max(lo, free_lo), my_hi = min(hi, free_hi);
   const bool cached = hi - lo <= kKeyCache;
-  auto key = [&](int i) { return cached ? s_keys[i - lo] : mass_key(mass[i]); };
-  // One more of a digit. The keys of a warp share few digits (weights of like size share their
-  // exponents), so equal ones are counted by one of their lanes.
+  auto key = [&](int i) { return cached ? s.keys[i - lo] : mass_key(mass[i]); };
+  // One more of a digit. Where many keys are alike (slots that were never attended weigh nothing), the
+  // warp's first key's digit is theirs: those are counted together.
   auto count = [&](unsigned* hist, bool on, unsigned digit) {
     const unsigned active = __ballot_sync(0xffffffffu, on);
     if (on) {
-      const unsigned same = __match_any_sync(active, digit);
-      if ((int)(__ffs(same) - 1) == lane) atomicAdd(&hist[digit], (unsigned)__popc(same));
+      const int first = __ffs(active) - 1;
+      const unsigned same = __ballot_sync(active, digit == __shfl_sync(active, digit, first));
+      if (!((same >> lane) & 1u)) atomicAdd(&hist[digit], 1u);
+      else if (lane == first) atomicAdd(&hist[digit], (unsigned)__popc(same));
     }
   };
 
-  // ---- before the first cluster barrier: page checks and the first digit's histogram ----
-  if (tid == 0) s_bad = 0u;
-  for (int i = tid; i < 512; i += kEvictThreads) s_hist[i >> 8][i & 255] = 0u;
+  // ---- page checks, keys and the range they span ----
+  if (tid == 0) s.bad = s.nfew = 0u;
+  for (int i = tid; i < 512; i += kEvictThreads) s.hist[i >> 8][i & 255] = 0u;
   __syncthreads();
   if (usable) {
     const int src_pages = (len + kPage - 1) / kPage, dst_pages = (keep + kPage - 1) / kPage;
     bool bad = false;
-    for (int i = rank * kEvictThreads + tid; i < src_pages; i += C * kEvictThreads)
+#pragma unroll 1
+    for (int i = part * kEvictThreads + tid; i < src_pages; i += parts * kEvictThreads)
       bad |= (unsigned)table[i] >= (unsigned)p.num_blocks;
-    for (int i = rank * kEvictThreads + tid; i < dst_pages; i += C * kEvictThreads)
+#pragma unroll 1
+    for (int i = part * kEvictThreads + tid; i < dst_pages; i += parts * kEvictThreads)
       bad |= (unsigned)dst_table[i] >= (unsigned)p.num_blocks;
-    if (bad) s_bad = 1u;
+    if (bad) s.bad = 1u;
   }
+  unsigned kmin = 0xffffffffu, kmax = 0u;
   if (select) {
-    for (int base = my_lo; base < my_hi; base += kEvictThreads) {
-      const int i = base + tid;
-      unsigned k = 0u;
-      if (i < my_hi) {
-        k = mass_key(mass[i]);
-        if (cached) s_keys[i - lo] = k;
-      }
-      count(s_hist[0], i < my_hi, k >> 24);
+#pragma unroll 4
+    for (int i = my_lo + tid; i < my_hi; i += kEvictThreads) {
+      const unsigned k = mass_key(mass[i]);
+      if (cached) s.keys[i - lo] = k;
+      kmin = min(kmin, k);
+      kmax = max(kmax, k);
+    }
+    warp_range(kmin, kmax);
+    if (lane == 0) {
+      s.wmin[warp] = kmin;
+      s.wmax[warp] = kmax;
     }
   }
   __syncthreads();
-  if (C > 1) cluster_sync();
-  bool bad_page = false;
-#pragma unroll
-  for (int r = 0; r < C; ++r) bad_page |= (C == 1 ? s_bad : dsmem_ld_u32(&s_bad, r)) != 0u;
+  if (select) {
+    kmin = s.wmin[lane % kEvictWarps];
+    kmax = s.wmax[lane % kEvictWarps];
+    warp_range(kmin, kmax);
+  }
+  bool bad_page = s.bad != 0u;
+  if constexpr (C > 1) {
+    if (!alone) {
+      if (tid == 0) {
+        s.kmin = kmin;
+        s.kmax = kmax;
+      }
+      __syncthreads();
+      cluster_sync();
+      const unsigned r = lane % C;
+      bad_page = __any_sync(0xffffffffu, dsmem_ld_u32(&s.bad, r) != 0u);
+      kmin = dsmem_ld_u32(&s.kmin, r);
+      kmax = dsmem_ld_u32(&s.kmax, r);
+      warp_range(kmin, kmax);
+    }
+  }
   const bool skip = !usable || bad_page;
-  // Every CTA of the cluster has read the length: the last of the sequence's KV heads to get
-  // here writes the new one (lens_out may be seq_lens).
-  if (rank == 0 && tid == 0) {
-    if (!gated && g == 0 && (bad_len || bad_page))
-      report(p.status, bad_len ? ODA_DEV_BAD_LEN : ODA_DEV_BAD_BLOCK);
-    if (ticket_arrive(&p.ticket[b]) == (unsigned)(p.hkv - 1)) {
+  if (tid == 0 && g == 0 && rank == 0) {
+    if (!gated && (bad_len || bad_page)) report(p.status, bad_len ? ODA_DEV_BAD_LEN : ODA_DEV_BAD_BLOCK);
+    if (!p.lens_alias) p.lens_out[b] = skip ? len : keep;
+  }
+  // In place, the last of the sequence's CTAs to have read the length writes the new one.
+  auto leave = [&]() {
+    if (p.lens_alias && tid == 0 && ticket_arrive(&p.ticket[b]) == (unsigned)(p.hkv * C - 1)) {
       p.ticket[b] = 0u;
       p.lens_out[b] = skip ? len : keep;
     }
-  }
+    if (!alone) cluster_sync();  // nobody leaves while its shared memory may still be read
+  };
   if (skip) {
-    if (C > 1) cluster_sync();  // nobody leaves while its shared memory may still be read
+    leave();
     return;
   }
 
   if (select) {
     unsigned need = p.budget - p.sink - p.recent;  // keys above the threshold stay, `need` of its equals
     unsigned threshold = 0xffffffffu;
-    if (need > 0) {
-      unsigned prefix = 0u;
+    if (need > 0 && kmin == kmax) {
+      threshold = kmin;
+    } else if (need > 0) {
+      int shift = 32 - __clz(kmin ^ kmax);  // above it all keys agree
+      unsigned prefix = shift < 32 ? kmin >> shift : 0u;
 #pragma unroll 1
-      for (int pass = 0; pass < 4; ++pass) {
-        unsigned* hist = s_hist[pass & 1];
-        const int shift = 24 - 8 * pass;
-        if (pass > 0) {
-          for (int base = my_lo; base < my_hi; base += kEvictThreads) {
-            const int i = base + tid;
-            const unsigned k = i < my_hi ? key(i) : 0u;
-            count(hist, i < my_hi && (k >> (shift + 8)) == prefix, (k >> shift) & 255u);
-          }
-          __syncthreads();
-          if (C > 1) cluster_sync();
-        }
-        {  // the cluster's histogram: thread (half, digit) sums half the CTAs' counts
-          unsigned n = 0u;
-          const int digit = tid & 255, half = tid >> 8;
-          if constexpr (C == 1) {
-            n = half == 0 ? hist[digit] : 0u;
-          } else {
-            unsigned v[C / 2];
-#pragma unroll
-            for (int r = 0; r < C / 2; ++r) v[r] = dsmem_ld_u32(&hist[digit], half * (C / 2) + r);
-#pragma unroll
-            for (int r = 0; r < C / 2; ++r) n += v[r];
-          }
-          s_half[tid] = n;
+      for (int pass = 0;; ++pass) {
+        unsigned* hist = s.hist[pass & 1];
+        const int bits = min(shift, 8), below = shift - bits;
+        const unsigned mask = (1u << bits) - 1u;
+#pragma unroll 1
+        for (int base = my_lo; base < my_hi; base += kEvictThreads) {
+          const int i = base + tid;
+          const unsigned k = i < my_hi ? key(i) : 0u;
+          const bool on = i < my_hi && (shift == 32 || (k >> shift) == prefix);
+          if (pass == 0) count(hist, on, (k >> below) & mask);
+          else if (on) atomicAdd(&hist[(k >> below) & mask], 1u);  // (few, and spread out)
         }
         __syncthreads();
-        if (warp == 0) {  // lane l: digits 8 l .. 8 l + 7; from the top
-          unsigned n[8], sum = 0u;
+        if (!alone) cluster_sync();
+        // Thread t < 256: digit 255 - t, counted over the cluster, and the keys above it.
+        unsigned n = 0u, upto = 0u;
+        if (tid < 256) {
+          const int digit = 255 - tid;
+          if (alone) {
+            n = hist[digit];
+          } else if constexpr (C > 1) {
+            unsigned v[C];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            n[i] = s_half[8 * lane + i] + s_half[256 + 8 * lane + i];
-            sum += n[i];
-          }
-          unsigned above = sum;  // keys in this lane's digits and the higher ones
+            for (int r = 0; r < C; ++r) v[r] = dsmem_ld_u32(&hist[digit], r);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const unsigned v = __shfl_down_sync(0xffffffffu, above, o);
-            if (lane + o < 32) above += v;
+            for (int r = 0; r < C; ++r) n += v[r];
           }
-          above -= sum;
-          if (above < need && above + sum >= need) {
-            unsigned a = above, here = 0u;
-            int d = 0;
-            bool found = false;
-#pragma unroll
-            for (int i = 7; i >= 0; --i) {
-              if (!found) {
-                if (a + n[i] >= need) {
-                  found = true;
-                  d = i;
-                  here = n[i];
-                } else {
-                  a += n[i];
-                }
-              }
-            }
-            s_digit = 8 * lane + d;
-            s_need = need - a;
-            s_all = here == need - a;  // every key of the digit stays: no lower digit matters
-          }
-        } else if (pass < 3 && tid >= kEvictThreads - 256) {
-          // the other histogram was last read before the cluster barrier above
-          if (pass > 0) s_hist[(pass + 1) & 1][tid - (kEvictThreads - 256)] = 0u;
+          upto = warp_scan(n, lane);
+          if (lane == 31) s.gt[warp] = upto;
+        } else {
+          // the other histogram was last read before the barrier above
+          s.hist[(pass + 1) & 1][tid - 256] = 0u;
         }
         __syncthreads();
-        prefix = (prefix << 8) | s_digit;
-        need = s_need;
-        if (s_all) {
-          threshold = (prefix << shift) - 1u;  // (not below 0: some free key does not stay)
-          need = 0u;
+        if (tid < 256) {
+#pragma unroll 1
+          for (int w = 0; w < warp; ++w) upto += s.gt[w];
+          if (upto - n < need && upto >= need) {
+            s.digit = 255 - tid;
+            s.need = need - (upto - n);
+            s.here = n;
+          }
+        }
+        __syncthreads();
+        prefix = (prefix << bits) | s.digit;
+        shift = below;
+        need = s.need;
+        if (s.here == need || shift == 0) {  // every key of the digit stays, or they are all equal
+          const bool all = s.here == need;
+          threshold = (prefix << shift) - (all ? 1u : 0u);  // (not below 0: some free key does not stay)
+          if (all) need = 0u;
           break;
         }
-        threshold = prefix;
+        if (s.here > kFew) continue;
+        // Few enough to be compared with one another: the threshold is the one with fewer than `need` keys
+        // above it and at least as many not below it.
+#pragma unroll 1
+        for (int i = my_lo + tid; i < my_hi; i += kEvictThreads) {
+          const unsigned k = key(i);
+          if ((k >> shift) == prefix) s.few[atomicAdd(&s.nfew, 1u)] = k;
+        }
+        __syncthreads();
+        unsigned mine = 0u;
+        int few = 0;
+        if (alone) {
+          few = (int)s.nfew;
+          if (tid < few) mine = s.few[tid];
+        } else if constexpr (C > 1) {
+          cluster_sync();
+#pragma unroll
+          for (int r = 0; r < C; ++r) {  // thread t: the cluster's t-th
+            const int nr = (int)dsmem_ld_u32(&s.nfew, r);
+            if (tid >= few && tid < few + nr) mine = dsmem_ld_u32(&s.few[tid - few], r);
+            few += nr;
+          }
+          cluster_sync();  // everyone has everyone's
+          if (tid < few) s.few[tid] = mine;
+          __syncthreads();
+        }
+        if (tid < few) {
+          unsigned above = 0u, same = 0u;
+#pragma unroll 4
+          for (int j = 0; j < few; ++j) {
+            above += s.few[j] > mine;
+            same += s.few[j] == mine;
+          }
+          if (above < need && above + same >= need) {  // (threads of equal keys write the same)
+            s.threshold = mine;
+            s.need = need - above;
+          }
+        }
+        __syncthreads();
+        threshold = s.threshold;
+        need = s.need;
+        break;
       }
     }
 
-    // ---- count, then list: warps take consecutive runs of this CTA's slots ----
-    const int per = ((hi - lo + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
-    const int wlo = min(hi, lo + warp * per), whi = min(hi, wlo + per);
+    // ---- count, then list: threads take consecutive runs of this CTA's slots (of odd length: the keys of a
+    // warp's lanes then lie in different banks) ----
+    const int per = ((hi - lo + kEvictThreads - 1) / kEvictThreads) | 1;
+    const int tlo = min(hi, lo + tid * per), thi = min(hi, tlo + per);
+    const bool choose = p.budget > p.sink + p.recent;
     auto classify = [&](int i, bool& above, bool& equal) {
-      above = equal = false;
-      if (i >= whi) return;
-      if (i < free_lo || i >= free_hi) {
-        above = true;
-      } else if (p.budget > p.sink + p.recent) {
+      above = i < free_lo || i >= free_hi;
+      equal = false;
+      if (!above && choose) {
         const unsigned k = key(i);
         above = k > threshold;
         equal = k == threshold;
       }
     };
     unsigned gt = 0u, eq = 0u;
-    for (int base = wlo; base < whi; base += 32) {
+#pragma unroll 1
+    for (int i = tlo; i < thi; ++i) {
       bool a, e;
-      classify(base + lane, a, e);
-      gt += __popc(__ballot_sync(0xffffffffu, a));
-      eq += __popc(__ballot_sync(0xffffffffu, e));
+      classify(i, a, e);
+      gt += a;
+      eq += e;
     }
-    if (lane == 0) {
-      s_gt[warp] = gt;
-      s_eq[warp] = eq;
+    // scans over the warp, then the warps before
+    unsigned gt_before = warp_scan(gt, lane), eq_before = warp_scan(eq, lane);
+    if (lane == 31) {
+      s.gt[warp] = gt_before;
+      s.eq[warp] = eq_before;
     }
+    gt_before -= gt;
+    eq_before -= eq;
     __syncthreads();
-    unsigned gt_before = 0u, eq_before = 0u;
-    for (int w = 0; w < kEvictWarps; ++w) {
-      if (w < warp) {
-        gt_before += s_gt[w];
-        eq_before += s_eq[w];
+#pragma unroll 1
+    for (int w = 0; w < warp; ++w) {
+      gt_before += s.gt[w];
+      eq_before += s.eq[w];
+    }
+    if (!alone) {
+      if (tid == kEvictThreads - 1) {
+        s.total[0] = gt_before + gt;
+        s.total[1] = eq_before + eq;
+      }
+      __syncthreads();
+      cluster_sync();
+#pragma unroll
+      for (int r = 0; r < C - 1; ++r) {
+        const unsigned gr = dsmem_ld_u32(&s.total[0], r), er = dsmem_ld_u32(&s.total[1], r);
+        gt_before += r < (int)rank ? gr : 0u;
+        eq_before += r < (int)rank ? er : 0u;
       }
     }
-    if (tid == kEvictThreads - 1) {
-      s_total[0] = gt_before + gt;
-      s_total[1] = eq_before + eq;
-    }
-    __syncthreads();
-    if (C > 1) cluster_sync();
-#pragma unroll
-    for (int r = 0; r < C - 1; ++r) {
-      const unsigned gr = dsmem_ld_u32(&s_total[0], r), er = dsmem_ld_u32(&s_total[1], r);
-      gt_before += r < (int)rank ? gr : 0u;
-      eq_before += r < (int)rank ? er : 0u;
-    }
-    for (int base = wlo; base < whi; base += 32) {
+#pragma unroll 1
+    for (int i = tlo; i < thi; ++i) {
       bool a, e;
-      classify(base + lane, a, e);
-      const unsigned am = __ballot_sync(0xffffffffu, a), em = __ballot_sync(0xffffffffu, e);
-      const unsigned below = (1u << lane) - 1u;
-      const unsigned my_eq = eq_before + __popc(em & below);
-      if (a || (e && my_eq < need))
-        kept[gt_before + __popc(am & below) + min(my_eq, need)] = base + lane;
-      gt_before += __popc(am);
-      eq_before += __popc(em);
+      classify(i, a, e);
+      if (a || (e && eq_before < need)) {
+        const unsigned at = gt_before + min(eq_before, need);
+        if (cached && alone) s.list[at] = (uint16_t)i;
+        else kept[at] = i;
+      }
+      gt_before += a;
+      eq_before += e;
     }
   } else {
+#pragma unroll 1
     for (int i = rank * kEvictThreads + tid; i < p.budget; i += C * kEvictThreads)
       kept[i] = i < len ? i : -1;
   }
-  if (C > 1) cluster_sync(); else __syncthreads();  // the whole list is written
+  if (alone) __syncthreads(); else cluster_sync();  // the whole list is written
+  if (select && cached && alone)
+#pragma unroll 1
+    for (int i = rank * kEvictThreads + tid; i < keep; i += C * kEvictThreads) kept[i] = s.list[i];
 
-  // ---- move ----
-  constexpr int kRowsPerRound = kEvictThreads * kPieces / Rows::kCount;
-  for (int base = 0; base < keep; base += C * kRowsPerRound) {
-    const int first = base + rank * kRowsPerRound;
-    const int rows = max(0, min(kRowsPerRound, keep - first));
+  // ---- move, in rounds of the cluster; the rows of the next round are looked up beside this one's copies ----
+  constexpr int kRound = kEvictThreads * kPieces / Rows::kCount < kEvictThreads
+                             ? kEvictThreads * kPieces / Rows::kCount
+                             : kEvictThreads;
+  const bool listed = cached && alone;
+  float m_next = 0.f;
+  auto lookup = [&](int base) {  // thread t: row base + rank * kRound + t
+    const int i = base + rank * kRound + tid;
+    if (tid < kRound && i < keep) {
+      const int from = !select ? i : listed ? (int)s.list[i] : kept[i];
+      const int buf = (base / (C * kRound)) & 1;
+      s.src[buf][tid] = (unsigned)table[from / kPage] * kPage + from % kPage;
+      s.dst[buf][tid] = (unsigned)dst_table[i / kPage] * kPage + i % kPage;
+      m_next = mass[from];
+    }
+  };
+  lookup(0);
+  __syncthreads();
+#pragma unroll 1
+  for (int base = 0; base < keep; base += C * kRound) {
+    const int first = base + rank * kRound, buf = (base / (C * kRound)) & 1;
+    const int rows = max(0, min(kRound, keep - first));
+    const float m = m_next;
     uint4 v[kPieces];
-    float m = 0.f;
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int e = tid + u * kEvictThreads;
-      if (e < rows * Rows::kCount) {
-        const int s = kept[first + e / Rows::kCount];
-        v[u] = *reinterpret_cast<const uint4*>(Rows::at(p, table[s / kPage], g, s % kPage, e % Rows::kCount));
-      }
+      if (e < rows * Rows::kCount)
+        v[u] = *reinterpret_cast<const uint4*>(Rows::at(p, s.src[buf][e / Rows::kCount], g, e % Rows::kCount));
     }
-    if (tid < rows) m = mass[kept[first + tid]];
+    lookup(base + C * kRound);
     if (p.in_place) {
       if (C > 1) cluster_sync(); else __syncthreads();
     }
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const int e = tid + u * kEvictThreads;
-      if (e < rows * Rows::kCount) {
-        const int i = first + e / Rows::kCount;
-        *reinterpret_cast<uint4*>(Rows::at(p, dst_table[i / kPage], g, i % kPage, e % Rows::kCount)) = v[u];
-      }
+      if (e < rows * Rows::kCount)
+        *reinterpret_cast<uint4*>(Rows::at(p, s.dst[buf][e / Rows::kCount], g, e % Rows::kCount)) = v[u];
     }
     if (tid < rows) mass_out[first + tid] = m;
+    __syncthreads();  // the next round's rows are looked up, this one's may be overwritten
   }
   // the slots given up weigh nothing until they are used again
+#pragma unroll 1
   for (int i = keep + rank * kEvictThreads + tid; i < len; i += C * kEvictThreads) mass_out[i] = 0.f;
-  if (C > 1) cluster_sync();  // nobody leaves while its shared memory may still be read
+  leave();
 }
 
 // CTAs per cluster: as many (at most 16) as keep all clusters within two waves of one CTA per SM,
@@ -351,12 +467,21 @@ static int prepare_evict(int device, int* most) {
   static int cached[64] = {0};
   if (device < 0 || device >= 64) return ODA_ERR_CUDA;
   if (cached[device] == 0) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(evict_kernel<Rows, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return cuda_status(e);
+    constexpr auto kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const int bytes = (int)sizeof(EvictSmem);
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(evict_kernel<Rows, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
+            cudaSuccess ||
+        (e = cudaFuncSetAttribute(evict_kernel<Rows, 16>, kSmem, bytes)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(evict_kernel<Rows, 8>, kSmem, bytes)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(evict_kernel<Rows, 4>, kSmem, bytes)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(evict_kernel<Rows, 2>, kSmem, bytes)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(evict_kernel<Rows, 1>, kSmem, bytes)) != cudaSuccess)
+      return cuda_status(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(16);
     cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = sizeof(EvictSmem);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 16;
@@ -379,6 +504,7 @@ static cudaError_t launch_evict_kernel(const EvictParams& p, long long rows, cud
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = sizeof(EvictSmem);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -449,6 +575,7 @@ static int launch_evict(const oda_kv* kv, const float* mass, int64_t mass_tokens
   p.lens_out = lens_out;
   p.ticket = static_cast<unsigned*>(ws);
   p.in_place = dst_table == kv->block_table || mass_out == mass;
+  p.lens_alias = lens_out == kv->seq_lens;
   p.status = kv->dev_status;
   const long long rows = (long long)kv->batch * kv->num_kv_heads;
   const int C = evict_cluster(di, rows, (long long)kv->max_blocks_per_seq * kPage, most);

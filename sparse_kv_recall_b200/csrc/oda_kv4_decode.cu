@@ -641,8 +641,11 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
       st.corr[1] += __shfl_xor_sync(0xffffffffu, st.corr[1], 2);
     }
     if (p.stats != nullptr) {
-      rows_vis = __reduce_add_sync(0xffffffffu, rows_vis);
-      pages_read = __reduce_add_sync(0xffffffffu, pages_read);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        rows_vis += __shfl_xor_sync(0xffffffffu, rows_vis, o);
+        pages_read += __shfl_xor_sync(0xffffffffu, pages_read, o);
+      }
       if (lane == 0 && (rows_vis | pages_read)) {
         atomicAdd(&s_rows, (unsigned long long)rows_vis);
         atomicAdd(&s_pages, (unsigned long long)pages_read);
