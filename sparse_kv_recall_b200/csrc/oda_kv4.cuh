@@ -57,14 +57,24 @@ __device__ __forceinline__ float2 f2_fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
+// The whole number nearest to a / s, halves to even, from a neighbour c of the quotient's.
+__device__ __forceinline__ float kv4_half(float a, float s, float c) {
+  const float e = fmaf(-c, s, a), twice = 2.f * fabsf(e);  // the remainder, exact
+  const bool odd = (static_cast<int>(c) & 1) != 0;
+  const float step = e > 0.f ? 1.f : -1.f;
+  return twice > s || (twice == s && odd) ? c + step : c;
+}
+
 // Quantise a row pair, one warp: lane = 16 * isv + li holds dims 8 li .. 8 li + 7 of the K (lanes
 // 0-15) or V row as bf16. Returns the lane's code word; `meta` is its group's word (the same in
 // the group's 8 lanes). m is the group's least value (a bf16 input value, so stored exactly), s
 // the bf16 next at or above (max - m) / 15, so that 15 s spans the group and every value is
-// within s / 2 of what it reads back as. The codes are rint((x - m) / s), division and all
-// roundings as IEEE fp32 has them: the product with the reciprocal is within 4e-6 of the quotient, so
-// only a value that close to a half needs the division itself. A group with an infinity or a NaN,
-// or whose span overflows, reads back as NaN.
+// within s / 2 of what it reads back as. The codes are rint((x - m) / s), halves to even, division and
+// all roundings as IEEE fp32 has them. They come from the product with the reciprocal, which is within
+// 4e-6 of the quotient; where that is as close to a half, twice the remainder is compared with s. That
+// decides as the division would: (k + 1/2) s has 13 bits, and a difference x - m that is not equal to it
+// is off by more than half an ulp of the quotient. A group with an infinity or a NaN, or whose span
+// overflows, reads back as NaN.
 __device__ __forceinline__ uint32_t kv4_quantise(const uint4& v, int lane, uint32_t& meta) {
   // the group's (max, -min) as a bf16 pair, NaN if any value is one
   constexpr uint32_t kSigns = 0x80008000u;
@@ -87,13 +97,18 @@ __device__ __forceinline__ uint32_t kv4_quantise(const uint4& v, int lane, uint3
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 a = f2_add(make_float2(bf16lo(w[i]), bf16hi(w[i])), make_float2(-m, -m));
-    // (a subnormal scale has no finite reciprocal: neither product's distance is then a number)
     const float2 t = f2_mul2(a, make_float2(inv, inv));
     c[i] = f2_add(f2_add(t, make_float2(kRound, kRound)), make_float2(-kRound, -kRound));
     const float2 d = f2_add(t, make_float2(-c[i].x, -c[i].y));
+    // (a subnormal scale has no finite reciprocal: neither product's distance is then a number)
     if (!(fmaxf(fabsf(d.x), fabsf(d.y)) < 0.49999f)) {
-      c[i].x = rintf(__fdiv_rn(a.x, s));
-      c[i].y = rintf(__fdiv_rn(a.y, s));
+      if (inv <= 3.4028234e38f) {
+        c[i].x = kv4_half(a.x, s, c[i].x);
+        c[i].y = kv4_half(a.y, s, c[i].y);
+      } else {
+        c[i].x = rintf(__fdiv_rn(a.x, s));
+        c[i].y = rintf(__fdiv_rn(a.y, s));
+      }
     }
   }
   // codes to nibbles: sums of whole numbers below 2^16, then below the exponent of 2^23

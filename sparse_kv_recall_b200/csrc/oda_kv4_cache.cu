@@ -67,7 +67,8 @@ __device__ __forceinline__ Slot find_slot(const RowsParams& p, int i, int g) {
   return s;
 }
 
-// The units of this warp: lane l < U finds unit l's row, head and slot, `at` hands them to the warp.
+// The units of this warp: lane l < U holds unit l's row and head, and after resolve() its slot; the others
+// ask for them.
 template <int U>
 struct Units {
   int i, g;
@@ -76,13 +77,15 @@ struct Units {
     const long long unit = ((long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5)) * U + (lane < U ? lane : 0);
     i = (int)(unit / p.hkv);
     g = (int)(unit % p.hkv);
+  }
+  __device__ __forceinline__ void resolve(const RowsParams& p, int lane) {
     slot.page = nullptr;
     slot.row = -1;
     if (lane < U && i < p.num_rows) slot = find_slot(p, i, g);
   }
-  __device__ __forceinline__ Slot at(int u, int& row_i, int& head) const {
-    row_i = __shfl_sync(0xffffffffu, i, u);
-    head = __shfl_sync(0xffffffffu, g, u);
+  __device__ __forceinline__ int row(int u) const { return __shfl_sync(0xffffffffu, i, u); }
+  __device__ __forceinline__ int head(int u) const { return __shfl_sync(0xffffffffu, g, u); }
+  __device__ __forceinline__ Slot at(int u) const {
     Slot s;
     s.page = reinterpret_cast<unsigned char*>(
         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(slot.page), u));
@@ -91,38 +94,36 @@ struct Units {
   }
 };
 
-constexpr int kInFlight = 4;
-
+// The rows are requested before their slots are looked up: neither needs the other.
 template <int U>
 __global__ void __launch_bounds__(kRowWarps * 32)
     kv4_append_kernel(const RowsParams p, const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
                       long long k_stride, long long v_stride) {
-  constexpr int N = U < kInFlight ? U : kInFlight;
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const Units<U> units(p, lane);
+  Units<U> units(p, lane);
   const __nv_bfloat16* base = (lane < 16 ? k_new : v_new) + 8 * (lane & 15);
   const long long stride = lane < 16 ? k_stride : v_stride;
+  uint4 v[U];
 #pragma unroll
-  for (int u0 = 0; u0 < U; u0 += N) {
-    Slot s[N];
-    uint4 v[N];
+  for (int u = 0; u < U; ++u) {
+    const int i = units.row(u), g = units.head(u);
+    v[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < p.num_rows) v[u] = *reinterpret_cast<const uint4*>(base + i * stride + g * kHeadDim);
+  }
+  units.resolve(p, lane);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      int i, g;
-      s[n] = units.at(u0 + n, i, g);
-      if (s[n].row >= 0) v[n] = *reinterpret_cast<const uint4*>(base + i * stride + g * kHeadDim);
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      if (s[n].row < 0) continue;  // (uniform)
-      uint32_t meta;
-      const uint32_t word = kv4_quantise(v[n], lane, meta);
-      kv4_store_row(s[n].page, s[n].row, word, meta, lane);
-    }
+  for (int u = 0; u < U; ++u) {
+    const Slot s = units.at(u);
+    if (s.row < 0) continue;  // (uniform)
+    uint32_t meta;
+    const uint32_t word = kv4_quantise(v[u], lane, meta);
+    kv4_store_row(s.page, s.row, word, meta, lane);
   }
 }
+
+constexpr int kInFlight = 4;
 
 template <int U, bool kBf16>
 __global__ void __launch_bounds__(kRowWarps * 32)
@@ -132,7 +133,8 @@ __global__ void __launch_bounds__(kRowWarps * 32)
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int li = lane & 15, isv = lane >> 4;
-  const Units<U> units(p, lane);
+  Units<U> units(p, lane);
+  units.resolve(p, lane);
   const int code_off = isv * kKv4VOff + 4 * kv4_word(li), meta_off = kKv4MetaOff + 4 * (lane >> 3);
 #pragma unroll
   for (int u0 = 0; u0 < U; u0 += N) {
@@ -141,10 +143,9 @@ __global__ void __launch_bounds__(kRowWarps * 32)
     bool ok[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      int i, g;
-      const Slot s = units.at(u0 + n, i, g);
+      const Slot s = units.at(u0 + n);
       ok[n] = s.row >= 0;
-      at[n] = ((size_t)i * p.hkv + g) * kHeadDim + 8 * li;
+      at[n] = ((size_t)units.row(u0 + n) * p.hkv + units.head(u0 + n)) * kHeadDim + 8 * li;
       if (ok[n]) {
         w[n] = *reinterpret_cast<const uint32_t*>(s.page + code_off + s.row * kKv4RowBytes);
         meta[n] = *reinterpret_cast<const uint32_t*>(s.page + meta_off + s.row * kKv4MetaBytes);

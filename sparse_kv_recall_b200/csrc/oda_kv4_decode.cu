@@ -135,19 +135,25 @@ constexpr float kNoMax = -1e30f;       // running maximum before any visible sco
 // factor that undoes q's power of two. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
 // word e = s / 2 of the lane's 16-byte code chunk, which is all group e & 1.
 template <int G>
-__device__ __forceinline__ float load_q4(const __nv_bfloat16* q, int lane, uint32_t (&b)[8][2],
-                                         float (&qs)[2]) {
+__device__ __forceinline__ void load_q4(const __nv_bfloat16* q, int lane, uint4 (&v)[4]) {
+  const int gid = lane >> 2, tig = lane & 3;
+  const int head = (gid >> 1) & (Roles<G>::kHeads - 1);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    v[e] = head < G ? *reinterpret_cast<const uint4*>(q + head * kHeadDim + 64 * (e & 1) +
+                                                      8 * (2 * tig + (e >> 1)))
+                    : make_uint4(0u, 0u, 0u, 0u);
+}
+template <int G>
+__device__ __forceinline__ float prepare_q4(const uint4 (&v)[4], int lane, uint32_t (&b)[8][2], float (&qs)[2]) {
   using R = Roles<G>;
   const int gid = lane >> 2, tig = lane & 3;
-  const int head = (gid >> 1) & (R::kHeads - 1), grp = gid & 1;
+  const int grp = gid & 1;
   float x[4][8];
   float top = 0.f, sum[2] = {0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (head < G)
-      v = *reinterpret_cast<const uint4*>(q + head * kHeadDim + 64 * (e & 1) + 8 * (2 * tig + (e >> 1)));
-    unpack8(v, x[e]);
+    unpack8(v[e], x[e]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       top = fmaxf(top, fabsf(x[e][k]));
@@ -566,8 +572,6 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
       piece.j0 = x - seg0;
       piece.x_end = min(share_end, seg0 + npg);
       piece.j1 = piece.j0 + (piece.x_end - x);
-      piece.first = cta_of(seg0, T, Pe);
-      piece.contrib = cta_of(seg0 + npg - 1, T, Pe) - piece.first + 1;
     }
     __syncthreads();
     const int b = piece.b, g = piece.g, bg = b * Hkv + g;
@@ -575,6 +579,8 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
     const int steps = pairs > warp ? (pairs - warp + kW4 - 1) / kW4 : 0;
     unsigned rows_vis = 0, pages_read = 0;  // this lane's pages
 
+    uint4 qv[4];
+    load_q4<G>(p.q + ((size_t)b * p.hq + g * G) * kHeadDim, lane, qv);  // (in flight beside the page table)
     auto fill = [&](int n0) {
       const int seen = kv4_refs(p, piece, refs, n0, warp, lane);
       rows_vis += seen & 255;
@@ -594,10 +600,14 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
       __syncwarp();
       issue(h);
     }
+    if (warp == kW4 - 1 && lane == 0) {  // (the warp with the fewest steps; needed at the merge)
+      piece.first = cta_of(x - piece.j0, T, Pe);
+      piece.contrib = cta_of(x - piece.j0 + (pre[b + 1] - pre[b]) / Hkv - 1, T, Pe) - piece.first + 1;
+    }
 
     uint32_t qb[8][2];
     float qs[2];
-    const float kq = load_q4<G>(p.q + ((size_t)b * p.hq + g * G) * kHeadDim, lane, qb, qs) * p.scale_log2;
+    const float kq = prepare_q4<G>(qv, lane, qb, qs) * p.scale_log2;
     float* scores = nullptr;
     if constexpr (kScores) scores = p.scores + ((size_t)b * p.hq + g * G) * p.cap;
 
