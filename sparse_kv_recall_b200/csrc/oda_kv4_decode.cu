@@ -199,6 +199,7 @@ __device__ __forceinline__ int rows_in_page(const SeqPlan& s, int pos) {
 // What a CTA works on: pages j0 .. j1 - 1 of the list of (sequence b, KV head g), units x .. x_end - 1 of the
 // flattened list; CTAs first .. first + contrib - 1 hold parts of this (b, g). In shared memory, filled in by
 // one thread: every warp's registers are spoken for.
+constexpr int kPlans4 = 32;  // plans of the first sequences, kept for the pieces
 struct Piece {
   SeqPlan plan;
   int b, g, j0, j1, x_end, first, contrib;
@@ -491,6 +492,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
   __shared__ int s_align, s_last;
   __shared__ unsigned long long s_rows, s_pages;
   __shared__ Piece piece;
+  __shared__ SeqPlan plans[kPlans4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   unsigned char* stages = smem + warp * kStages4 * kStageBytes4;
@@ -512,6 +514,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
   for (int b = tid; b < B; b += kThreads4) {
     const SeqPlan sp = make_plan(p.plan, b);
     pre[b + 1] = sp.npages * Hkv;
+    if (b < kPlans4) plans[b] = sp;
     if (cta == 0 && sp.err != 0) report(p.status, sp.err);
   }
   __syncthreads();
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
         if (pre[mid] <= x) lo = mid; else hi = mid - 1;
       }
       const int npg = (pre[lo + 1] - pre[lo]) / Hkv;
-      piece.plan = make_plan(p.plan, lo);
+      piece.plan = lo < kPlans4 ? plans[lo] : make_plan(p.plan, lo);
       piece.b = lo;
       piece.g = (x - pre[lo]) / npg;
       const int seg0 = pre[lo] + piece.g * npg;
