@@ -416,9 +416,10 @@ def make_kv4(cache, block_table, seq_lens, dev_status=None, stats=None) -> oda_k
     return kv
 
 
-# These wrappers run once a layer and step, so their checks are few attribute reads: a tensor's device,
-# type, contiguity and shape, and its address.
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+# These wrappers run once a layer and step, where the call itself takes longer than a small kernel, so
+# their checks are few attribute reads: a tensor's shape, device, type, contiguity, and its address.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 
 
@@ -431,27 +432,30 @@ def _at(t, dev: int, dtype, shape, name):
     """Address of a contiguous tensor of the given type and shape on device `dev` (None: of None)."""
     if t is None:
         return None
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.get_device() != dev:
-        _wrong_device(t, dev, name)
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    if (shape is not None and t.shape != shape) or t.get_device() != dev or \
+            (dtype is not None and t.dtype is not dtype) or not t.is_contiguous():
+        _refuse(t, dev, dtype, shape, name)
     return t.data_ptr()
 
 
-def _wrong_device(t, dev, name):
+def _refuse(t, dev, dtype, shape, name):
+    if shape is not None:
+        _shape(t, shape, name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    raise ValueError("%s must be on the cache's device cuda:%d, got %s" % (name, dev, t.device))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the cache's device cuda:%d, got %s" % (name, dev, t.device))
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _kv_device(kv) -> int:
     """The device of a cache made by make_kv / make_kv4 (the current one for a handle made by hand)."""
-    refs = getattr(kv, "_refs", None)
-    return refs[0].get_device() if refs else (torch.cuda.current_device() if torch.cuda.is_available() else 0)
+    try:
+        return kv._refs[0].get_device()
+    except AttributeError:
+        return torch.cuda.current_device() if torch.cuda.is_available() else 0
 
 
 def _call(fn_name, kv, dev, stream, *args):
@@ -464,7 +468,7 @@ def _call(fn_name, kv, dev, stream, *args):
         st = _raw_stream(dev)
     else:
         st = torch.cuda.current_stream(dev).cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _get_device():
         rc = fn(kv, *args, st)
     else:
         with torch.cuda.device(dev):
@@ -475,17 +479,16 @@ def _call(fn_name, kv, dev, stream, *args):
 
 def _row_stride(t, hkv: int, dev: int, name) -> int:
     """Element stride of bf16 rows [n][hkv][128] whose heads and dims are dense."""
-    n, h, d = t.shape if t.dim() == 3 else (0, 0, 0)
-    if h != hkv or d != 128:
-        raise ValueError("%s must have shape (rows, %d, 128), got %s" % (name, hkv, tuple(t.shape)))
-    if t.get_device() != dev:
-        _wrong_device(t, dev, name)
-    if t.dtype is not _BF16:
-        raise ValueError("%s must be %s, got %s" % (name, _BF16, t.dtype))
-    s = t.stride()
-    if s[2] != 1 or (hkv > 1 and s[1] != 128):
+    shape = t.shape
+    n = shape[0]
+    if shape != (n, hkv, 128):
+        raise ValueError("%s must have shape (rows, %d, 128), got %s" % (name, hkv, tuple(shape)))
+    if t.get_device() != dev or t.dtype is not _BF16:
+        _refuse(t, dev, _BF16, None, name)
+    s, h, d = t.stride()
+    if d != 1 or (hkv > 1 and h != 128):
         raise ValueError("%s: heads and dims must be dense" % name)
-    return s[0] if n > 1 else max(s[0], hkv * 128)
+    return s if n > 1 else max(s, hkv * 128)
 
 
 def _cu_rows(kv, cu_rows, num_rows, dev):
