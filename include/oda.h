@@ -327,7 +327,8 @@ int oda_kv4_read(const oda_kv4* kv, void* k_out, void* v_out, int32_t out_dtype,
 /* Decode attention over the 4-bit cache under any rule (arguments and results as oda_decode; k_new,
  * v_new dense bf16 [batch][num_kv_heads][128] are quantised into slot t and attended as they read
  * back). Weights, sums and the output are fp32 until the last rounding. ws: at least
- * oda_kv4_decode_workspace_size() bytes, zeroed once, as for the other decode calls. */
+ * oda_kv4_decode_workspace_size() bytes, zeroed once, as for the other decode calls; calls that
+ * may overlap on the GPU need a workspace each. */
 int oda_kv4_decode_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
                                   size_t* bytes);
 int oda_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q, int32_t num_q_heads,
@@ -344,7 +345,8 @@ int oda_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q, 
  * mass_tokens a multiple of 4 and at least 16 * max_blocks_per_seq. mass_in may be mass_out (only
  * visible positions are then touched) or NULL (zero); it may not overlap it otherwise. ws: at least the
  * matching workspace size (it holds a score per query head and position), zeroed once. With a keep list
- * that is not strictly ascending the sequence's mass is unspecified. Two kernel launches. */
+ * that is not strictly ascending the sequence's mass is unspecified. Calls that may overlap on the GPU need
+ * a workspace each. Two kernel launches. */
 int oda_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
                                    int32_t max_blocks_per_seq, size_t* bytes);
 int oda_kv4_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
@@ -360,19 +362,21 @@ int oda_kv4_decode_mass(const oda_kv4* kv, const oda_visibility* vis, const void
 
 /* Evict: every sequence of more than `budget` tokens is cut down to `budget`. Each KV head keeps its
  * first `sink` slots, its last `recent` slots, and of the others the budget - sink - recent of the largest
- * mass (ties to the lower slot; -0 counts as 0), in ascending slot order, as slots 0 .. budget - 1 of the
- * destination pages dst_block_table (int32 [batch][dst_blocks_per_seq], page ids of the same cache,
- * holding min(budget, 16 * max_blocks_per_seq) tokens at least). Shorter sequences keep every slot.
+ * mass (ties to the lower slot; -0 counts as 0, a NaN above every number), in ascending slot order, as
+ * slots 0 .. budget - 1 of the destination pages dst_block_table (int32 [batch][dst_blocks_per_seq], page
+ * ids of the same cache, holding min(budget, 16 * max_blocks_per_seq) tokens at least). Shorter sequences
+ * keep every slot.
  *   kept         : int32 [batch][num_kv_heads][budget], the old slot of every kept one, then -1
  *   mass_out     : fp32 [batch][num_kv_heads][mass_tokens]: the kept slots' mass, then 0 up to the old length
  *   seq_lens_out : int32 [batch], the new lengths
- * In place: dst_block_table may be kv->block_table (dst_blocks_per_seq is then max_blocks_per_seq),
- * mass_out may be mass, seq_lens_out may be kv->seq_lens. Otherwise destination pages are no pages of
- * any sequence's history. No page may belong to two sequences of the batch that are written. A sequence
- * with gate[b] == 0 (gate nullable), a bad length (ODA_DEV_BAD_LEN) or a bad page id in either table
- * (ODA_DEV_BAD_BLOCK) is left as it is, with its old length in seq_lens_out. sink, recent >= 0,
- * sink + recent <= budget, budget >= 1, mass_tokens >= 16 * max_blocks_per_seq. ws:
- * oda_kv_evict_workspace_size() bytes, zeroed once; left zeroed. */
+ * In place: dst_block_table may be kv->block_table (dst_blocks_per_seq is then max_blocks_per_seq) or hold
+ * the same pages at the same places, mass_out may be mass, seq_lens_out may be kv->seq_lens. Otherwise
+ * destination pages are no pages of any sequence's history. No page may belong to two sequences of the
+ * batch that are written. A sequence with gate[b] == 0 (gate nullable), a bad length (ODA_DEV_BAD_LEN) or
+ * a bad page id in either table (ODA_DEV_BAD_BLOCK) is left as it is, with its old length in seq_lens_out.
+ * sink, recent >= 0, sink + recent <= budget, budget >= 1, mass_tokens >= 16 * max_blocks_per_seq. ws:
+ * oda_kv_evict_workspace_size() bytes, zeroed once; left zeroed; calls that may overlap on the GPU need one
+ * each. */
 int oda_kv_evict_workspace_size(int32_t batch, size_t* bytes);
 int oda_kv_evict(const oda_kv* kv, const float* mass, int64_t mass_tokens, int32_t sink, int32_t recent,
                  int32_t budget, const int32_t* gate, const int32_t* dst_block_table,

@@ -29,6 +29,7 @@ namespace oda {
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kPieces = 8;  // 16-byte pieces a thread moves per round
+static_assert(kEvictThreads == 512, "threads 0-255 take a digit each, 256-511 clear the other histogram");
 
 struct EvictParams {
   unsigned char* k_cache;  // 4-bit: the codes; v_cache unused
@@ -46,7 +47,7 @@ struct EvictParams {
   int32_t* kept;
   int32_t* lens_out;
   unsigned* ticket;   // [batch], used with lens_alias
-  int in_place;       // the destination may be the source: order loads before stores
+  int in_place;       // the destination is the source: order loads before stores
   int lens_alias;     // lens_out is seq_lens
   int* status;
 };
@@ -74,8 +75,9 @@ __device__ __forceinline__ unsigned dsmem_ld_u32(const unsigned* local, unsigned
   return __float_as_uint(dsmem_ld(reinterpret_cast<const float*>(local), rank));
 }
 
-// Ascending order of floats as unsigned integers; -0 counts as 0.
+// Ascending order of floats as unsigned integers; -0 counts as 0, a NaN above everything.
 __device__ __forceinline__ unsigned mass_key(float m) {
+  if (isnan(m)) return 0xffffffffu;
   const unsigned u = __float_as_uint(m + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
@@ -107,7 +109,7 @@ struct EvictSmem {
   unsigned keys[kKeyCache];
   uint16_t list[kAlone];      // alone: the kept slots
   unsigned hist[2][256];
-  unsigned bad, digit, need, here, kmin, kmax, threshold;
+  unsigned bad, in_place, digit, need, here, kmin, kmax, threshold;
   unsigned few[kFew], nfew;   // keys of the digit that holds the threshold, once they are few
   unsigned wmin[kEvictWarps], wmax[kEvictWarps];
   unsigned gt[kEvictWarps], eq[kEvictWarps], total[2];
@@ -162,14 +164,17 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
   __syncthreads();
   if (usable) {
     const int src_pages = (len + kPage - 1) / kPage, dst_pages = (keep + kPage - 1) / kPage;
-    bool bad = false;
+    bool bad = false, same = false;  // (a destination table may be a copy of the source's)
 #pragma unroll 1
     for (int i = part * kEvictThreads + tid; i < src_pages; i += parts * kEvictThreads)
       bad |= (unsigned)table[i] >= (unsigned)p.num_blocks;
 #pragma unroll 1
-    for (int i = part * kEvictThreads + tid; i < dst_pages; i += parts * kEvictThreads)
+    for (int i = part * kEvictThreads + tid; i < dst_pages; i += parts * kEvictThreads) {
       bad |= (unsigned)dst_table[i] >= (unsigned)p.num_blocks;
-    if (bad) s.bad = 1u;
+      same |= dst_table[i] == table[i];
+    }
+    if (bad) atomicOr(&s.bad, 1u);
+    if (same) atomicOr(&s.bad, 2u);
   }
   unsigned kmin = 0xffffffffu, kmax = 0u;
   if (select) {
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
     kmax = s.wmax[lane % kEvictWarps];
     warp_range(kmin, kmax);
   }
-  bool bad_page = s.bad != 0u;
+  unsigned flags = s.bad;
   if constexpr (C > 1) {
     if (!alone) {
       if (tid == 0) {
@@ -202,13 +207,17 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
       __syncthreads();
       cluster_sync();
       const unsigned r = lane % C;
-      bad_page = __any_sync(0xffffffffu, dsmem_ld_u32(&s.bad, r) != 0u);
+      flags = dsmem_ld_u32(&s.bad, r);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) flags |= __shfl_xor_sync(0xffffffffu, flags, o);
       kmin = dsmem_ld_u32(&s.kmin, r);
       kmax = dsmem_ld_u32(&s.kmax, r);
       warp_range(kmin, kmax);
     }
   }
+  const bool bad_page = (flags & 1u) != 0u;
   const bool skip = !usable || bad_page;
+  if (tid == 0) s.in_place = p.in_place || (flags & 2u) != 0u;  // (the same all over the cluster)
   if (tid == 0 && g == 0 && rank == 0) {
     if (!gated && (bad_len || bad_page)) report(p.status, bad_len ? ODA_DEV_BAD_LEN : ODA_DEV_BAD_BLOCK);
     if (!p.lens_alias) p.lens_out[b] = skip ? len : keep;
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
         v[u] = *reinterpret_cast<const uint4*>(Rows::at(p, s.src[buf][e / Rows::kCount], g, e % Rows::kCount));
     }
     lookup(base + C * kRound);
-    if (p.in_place) {
+    if (s.in_place) {
       if (C > 1) cluster_sync(); else __syncthreads();
     }
 #pragma unroll
@@ -530,7 +539,8 @@ static int evict_args(const oda_kv* kv, const float* mass, int64_t mass_tokens, 
   if ((long long)dst_blocks * kPage < budget && (long long)dst_blocks * kPage < cap)
     return ODA_ERR_INVALID_ARG;  // a destination shorter than what may be kept
   if (dst_table == kv->block_table && dst_blocks != kv->max_blocks_per_seq) return ODA_ERR_INVALID_ARG;
-  if (cap >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
+  // (slots and rounds of slots are counted in 32 bits)
+  if (cap > (1ll << 31) - (1 << 16) || budget > (1ll << 31) - (1 << 16)) return ODA_ERR_UNSUPPORTED_SHAPE;
   if (kv->batch == 0) return ODA_OK;
   if (mass == nullptr || dst_table == nullptr || kept == nullptr || mass_out == nullptr ||
       lens_out == nullptr || ws == nullptr)

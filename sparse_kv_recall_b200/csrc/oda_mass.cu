@@ -136,7 +136,7 @@ static int decode_mass(const oda_kv* kv, const oda_kv4* kv4, const oda_visibilit
     return rc;
   const long long cap = (long long)kv->max_blocks_per_seq * kPage;
   if (mass_tokens < cap || mass_tokens % 4 != 0) return ODA_ERR_INVALID_ARG;
-  if (cap >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
+  if (cap > (1ll << 31) - (1 << 16)) return ODA_ERR_UNSUPPORTED_SHAPE;  // (positions are counted in 32 bits)
   if (kv->batch == 0) return ODA_OK;
   if (mass_out == nullptr || !aligned_or_null(mass_out, 16) || !aligned_or_null(mass_in, 16))
     return ODA_ERR_INVALID_ARG;

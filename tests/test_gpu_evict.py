@@ -214,6 +214,14 @@ def test_evict_orders_every_kind_of_weight(kv4):
     """Equal weights, zeros of both signs, infinities, subnormals and negative numbers."""
     c = PagedCase([64], 1, 1, seed=130, kv4=kv4)
     vals = [0.0, -0.0, 1.0, 1.0, float("inf"), -1.0, 2.0 ** -140, -2.0 ** -140, float("-inf"), 3.0]
+    nan = torch.tensor([0x7fc00000, 0xffc00000 - (1 << 32)], dtype=torch.int32, device="cuda").view(torch.float32)
+    for budget in (2, 4, 20):                      # a NaN of either sign counts above everything
+        m = torch.zeros((1, 1, 64), device="cuda")
+        m[0, 0, 20], m[0, 0, 40], m[0, 0, 50] = nan[1], nan[0], float("inf")
+        c = PagedCase([64], 1, 1, seed=130, kv4=kv4)
+        kept, _, _ = _evict(c, m, 0, 0, budget)
+        c.ok()
+        assert kept[0, 0].tolist() == sorted(([20, 40, 50] + [i for i in range(64) if i not in (20, 40, 50)])[:budget])
     mass = torch.tensor([(vals * 7)[:64]], device="cuda").view(1, 1, 64).contiguous()
     for budget in (1, 6, 7, 8, 13, 20, 21, 33, 40, 48, 63):
         m = mass.clone()
@@ -221,6 +229,18 @@ def test_evict_orders_every_kind_of_weight(kv4):
         kept, _, _ = _evict(c2, m, 0, 0, budget)
         c2.ok()
         assert kept[0, 0].tolist() == K.kept_slots(mass[0, 0].tolist(), 64, 0, 0, budget).tolist(), budget
+
+
+@BOTH
+@pytest.mark.parametrize("n,hkv,budget", [(700, 2, 333), (20000, 1, 9000)])
+def test_evict_into_a_copy_of_the_table_is_in_place(kv4, n, hkv, budget):
+    """The destination holds the source's own pages but is another tensor, as are the weights and lengths."""
+    c = PagedCase([n, n - 9], hkv, hkv, seed=129, kv4=kv4)
+    mass = _random_mass(c, 128)
+    old, old_mass = (c.k.copy(), c.v.copy()), mass.clone()
+    kept, mass_out, new_lens = _evict(c, mass, 4, 50, budget, c.bt[:, :-(-budget // 16)].contiguous())
+    c.ok()
+    _assert_evicted(c, [n, n - 9], c.bt, old, old_mass, kept, mass_out, new_lens, 4, 50, budget)
 
 
 @BOTH

@@ -86,6 +86,7 @@ def test_decode_mass_checks(lib, name, make):
     assert call(mass_out=None) == I and call(mass_out=0x80004) == I and call(mass_in=0x90008) == I
     assert call(ws=0x60001) == I and call(kv=make(batch=0)) == OK
     assert call(kv=make(max_blocks_per_seq=1 << 27, num_kv_heads=4, batch=1), tokens=1 << 31) == U
+    assert call(kv=make(max_blocks_per_seq=(1 << 27) - 1, num_kv_heads=4, batch=1), tokens=1 << 31) == U
     n = ctypes.c_size_t(0)
     size = getattr(lib, name + "_workspace_size")
     assert size(2, 8, 16, 0, ctypes.byref(n)) == I and size(2, 8, 12, 4, ctypes.byref(n)) == U
@@ -107,6 +108,8 @@ def test_evict_checks(lib, name, make):
         assert call(**{null: None}) == I
     assert call(mass=0x80002) == I and call(gate=0x2002) == I and call(kept=0xa0001) == I and call(ws=0xd0004) == I
     assert call(nbytes=4) == W
+    assert call(kv=make(max_blocks_per_seq=(1 << 27) - 1, num_kv_heads=4, batch=1), tokens=1 << 31) == U
+    assert call(budget=2 ** 31 - 1, blocks=1 << 27) == U
     assert call(kv=make(batch=0)) == OK and call(kv=make(num_blocks=0)) == I
     n = ctypes.c_size_t(0)
     assert lib.oda_kv_evict_workspace_size(-1, ctypes.byref(n)) == I
