@@ -629,13 +629,13 @@ __device__ __forceinline__ void decode_pass(const DecodeParams& p, const SplitSm
         }
         if constexpr (kScores) {
           // Rows that are not visible may hold anything: a weight of zero times a NaN is a NaN.
-          bool hidden = false;
-          for (int row = 0; row < kPage; ++row) {
-            if (row_visible(sp, r.lp * kPage + row)) continue;
-            hidden = true;
-            *reinterpret_cast<uint2*>(st + kPageBytes + row * kRowBytes + 8 * lane) = make_uint2(0u, 0u);
-          }
-          if (hidden) {
+          const int pos = r.lp * kPage;
+          if (pos < sp.row_lo || pos + kPage - 1 > sp.row_hi ||
+              (pos + kPage > sp.gap_lo && pos < sp.gap_hi)) {
+#pragma unroll 1
+            for (int row = 0; row < kPage; ++row)
+              if (!row_visible(sp, pos + row))
+                *reinterpret_cast<uint2*>(st + kPageBytes + row * kRowBytes + 8 * lane) = make_uint2(0u, 0u);
             fence_proxy_async_smem();  // this stage is refilled by a bulk copy later
             __syncwarp();
           }
