@@ -215,6 +215,7 @@ static int rows_params(const oda_kv4* kv, int32_t num_rows, const int32_t* cu_ro
   if (num_rows < 0 || (cu_rows == nullptr && num_rows != kv->batch)) return ODA_ERR_INVALID_ARG;
   if (!aligned_or_null(cu_rows, 4) || !aligned_or_null(gate, 4)) return ODA_ERR_INVALID_ARG;
   if (kv->batch == 0 || num_rows == 0) return ODA_OK;
+  if (num_rows > 0x7fff0000) return ODA_ERR_UNSUPPORTED_SHAPE;  // (the last warps' rows pass num_rows)
   const long long units = (long long)num_rows * kv->num_kv_heads;
   *many = units >= kManyUnits;
   const long long per_cta = kRowWarps * (*many ? 8 : 1);

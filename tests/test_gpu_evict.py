@@ -389,3 +389,72 @@ def test_a_run_of_decode_steps_with_eviction(kv4):
                     rows[b][g] = [rows[b][g][p] for p in keep_]
                     want_mass[b][g] = [want_mass[b][g][p] for p in keep_]
     assert evicted >= 2
+
+
+@BOTH
+def test_mass_and_evict_at_once_and_graphs_over_one_workspace(kv4):
+    """Two calls at once on two streams, a workspace each; then two graphs of different rules over one
+    workspace, replayed in turn."""
+    c = PagedCase([2600, 700, 31], 8, 4, seed=150, kv4=kv4, spare=6 * 20)
+    mass_call, ev = _mass_call(c), oda.oda_kv4_evict if kv4 else oda.oda_kv_evict
+    before = _random_mass(c, 151)
+    side = torch.cuda.Stream()
+
+    def buffers(i):
+        return dict(out=c.out(), mass=torch.zeros_like(before), mass2=torch.zeros_like(before), ws=torch.zeros_like(c.ws),
+                    kept=torch.zeros((3, 4, 300), dtype=torch.int32, device="cuda"), lens=torch.zeros_like(c.seq_lens),
+                    dst=c.spare[60 * i:60 * i + 60].view(3, 20).contiguous(),
+                    ews=torch.zeros(oda.oda_kv_evict_workspace_size(3), dtype=torch.uint8, device="cuda"))
+
+    def step(s, vis, stream=None):
+        mass_call(c.kv, vis, c.q, SCALE, s["out"][0], s["ws"], s["mass"], mass_in=before, lse=s["out"][1],
+                  stream=stream)
+        ev(c.kv, s["mass"], 2, 20, 300, s["dst"], s["kept"], s["mass2"], s["lens"], s["ews"], stream=stream)
+
+    def results(s):
+        return [x.clone() for x in (*s["out"], s["mass"], s["mass2"], s["kept"], s["lens"])]
+    a, b = buffers(0), buffers(1)
+    step(a, full())
+    torch.cuda.synchronize()
+    want = results(a)
+    for _ in range(10):
+        step(a, full())
+        step(b, full(), stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for s in (a, b) for x, y in zip(results(s), want))
+    c.ok()
+    step(b, local(4, 100))
+    torch.cuda.synchronize()
+    wants = [want, results(b)]
+    b["ws"], b["ews"] = a["ws"], a["ews"]
+    graphs = []
+    for s, vis in ((a, full()), (b, local(4, 100))):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(s, vis)
+        graphs.append(g)
+    for i in (1, 0, 0, 1, 0, 1):
+        s = (a, b)[i]
+        for x in (*s["out"], s["mass"], s["mass2"], s["kept"], s["lens"]):
+            x.zero_()
+        graphs[i].replay()
+        c.ok()
+        assert all(torch.equal(x, y) for x, y in zip(results(s), wants[i]))
+
+
+@BOTH
+def test_sequences_that_share_a_prefix_are_cut_apart(kv4):
+    """Three sequences over the same first pages, evicted into pages of their own."""
+    lens, hkv, budget = [500, 500, 420], 2, 64
+    c = PagedCase(lens, hkv, hkv, seed=152, kv4=kv4, spare=3 * 4)
+    c.bt[1, :20] = c.bt[0, :20]
+    c.bt[2, :20] = c.bt[0, :20]
+    c.snapshot()
+    mass = _random_mass(c, 153)
+    old, old_mass, raw = (c.k.copy(), c.v.copy()), mass.clone(), c.raw()
+    dst = c.spare.view(3, 4).contiguous()
+    kept, mass_out, new_lens = _evict(c, mass, 4, 16, budget, dst)
+    c.ok()
+    _assert_evicted(c, lens, dst, old, old_mass, kept, mass_out, new_lens, 4, 16, budget)
+    src = torch.unique(c.bt[c.bt >= 0]).long()
+    assert torch.equal(c.raw()[src], raw[src]) if kv4 else torch.equal(c.raw()[:, src], raw[:, src])

@@ -46,6 +46,29 @@ def test_append_and_read_match_the_oracle_exactly(hkv, lengths):
         at += n
 
 
+def test_append_and_read_of_many_rows_take_eight_at_a_time():
+    """Enough (row, KV head) pairs for the warps of eight, an odd number of them, sequences that end inside
+    such a group, one gated off."""
+    lengths, hkv = [3000, 1, 17, 8192, 5, 250], 7
+    n = sum(lengths)
+    assert n * hkv > 8 * 8 * 8 * 148 and n * hkv % 8 != 0
+    rows = [gauss((n, hkv, 128), 55 + i, 2.0) - i for i in range(2)]
+    c = PagedCase(lengths, hkv, hkv, seed=57, rows=rows)
+    k, v = _read_all(c)
+    ref = [K.round_trip(x.double().cpu().numpy()).astype(np.float32) for x in rows]
+    assert np.array_equal(k.cpu().numpy(), ref[0]) and np.array_equal(v.cpu().numpy(), ref[1])
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    gate = torch.tensor([1, 0, 1, 0, 1, 1], dtype=torch.int32, device="cuda")
+    oda.oda_kv4_append(c.kv, rows[1], rows[0], cu_rows=cu, gate=gate)
+    k, v = _read_all(c)
+    at = 0
+    for b, m in enumerate(lengths):
+        r = slice(at, at + m)
+        kk, vv = (ref[1], ref[0]) if b not in (1, 3) else (ref[0], ref[1])
+        assert np.array_equal(k[r].cpu().numpy(), kk[r]) and np.array_equal(v[r].cpu().numpy(), vv[r])
+        at += m
+
+
 def test_append_takes_rows_out_of_a_fused_projection_and_leaves_the_rest():
     """Strided rows; ranges that are empty, shorter than the sequence, and rows behind the last range
     or gated off: every other byte of the cache keeps its contents."""
@@ -385,3 +408,62 @@ def test_repeatable_on_streams_and_in_graphs():
         c.snapshot()
         r, rl, _ = c.oracle(lambda b, t: O.local_positions(t, 4, 100))
         assert_out_close(out, r)
+
+
+def test_two_graphs_share_a_workspace_and_sequences_share_pages():
+    """Graphs of a Full and a Local call over one workspace, replayed in turn; sequences 1 and 2 are the
+    same pages, sequence 2 shorter by some."""
+    c = PagedCase([2500, 700, 600, 40], 16, 4, seed=90)
+    c.bt[2] = c.bt[1]
+    c.bt_h = c.bt.cpu().numpy()
+    outs = [c.out(), c.out()]
+    vis = [full(), local(4, 256)]
+    graphs = []
+    for (out, lse), v in zip(outs, vis):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            oda.oda_kv4_decode(c.kv, v, c.q, SCALE, out, c.ws, lse=lse)
+        graphs.append(g)
+    positions = [lambda b, t: O.full_positions(t), lambda b, t: O.local_positions(t, 4, 256)]
+    for i in (0, 1, 1, 0, 1, 0):
+        out, lse = outs[i]
+        out.fill_(float("nan"))
+        graphs[i].replay()
+        c.ok()
+        ref, rlse, _ = c.oracle(positions[i])
+        assert_out_close(out, ref)
+        assert_lse_close(lse.cpu().numpy(), rlse)
+
+
+def test_calls_one_behind_the_other_see_each_others_writes():
+    """Append, decode, append, decode without a host wait: a launch may begin before its predecessor ends, but
+    reads nothing of it before."""
+    c = PagedCase([300, 16, 33], 8, 4, seed=91)
+    rows = [(gauss(c.k_new.shape, 300 + i), gauss(c.k_new.shape, 400 + i)) for i in range(12)]
+    got = [c.out() for _ in rows]
+    back = [(torch.empty(3, 4, 128, device="cuda"), torch.empty(3, 4, 128, device="cuda")) for _ in rows]
+    torch.cuda.synchronize()
+    for (k, v), (out, lse), (rk, rv) in zip(rows, got, back):
+        oda.oda_kv4_append(c.kv, k, v)
+        oda.oda_kv4_decode(c.kv, full(), c.q, SCALE, out, c.ws, lse=lse)
+        oda.oda_kv4_read(c.kv, rk, rv)
+    c.ok()
+    for (k, v), (out, lse), (rk, rv) in zip(rows, got, back):
+        assert np.array_equal(rk.cpu().numpy(), K.round_trip(k.double().cpu().numpy()).astype(np.float32))
+        assert np.array_equal(rv.cpu().numpy(), K.round_trip(v.double().cpu().numpy()).astype(np.float32))
+        c.k_new, c.v_new = k, v
+        ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t), commit=True)
+        assert_out_close(out, ref)
+        assert_lse_close(lse.cpu().numpy(), rlse)
+
+
+def test_one_sequence_of_many_ctas_for_each_head_count():
+    """A long history on every head grouping: the partials of some hundred CTAs are merged in chunks."""
+    for G, hkv in ((1, 1), (2, 1), (4, 1), (4, 2)):
+        c = PagedCase([40000], G * hkv, hkv, seed=92 + G)
+        out, lse = c.out()
+        oda.oda_kv4_decode(c.kv, full(), c.q, SCALE, out, c.ws, lse=lse)
+        c.ok()
+        ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t))
+        assert_out_close(out, ref, "G %d hkv %d" % (G, hkv))
+        assert_lse_close(lse.cpu().numpy(), rlse)

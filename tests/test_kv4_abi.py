@@ -49,6 +49,7 @@ def test_append_and_read_checks(lib):
         assert call(k=None) == I and call(v=0x2008) == I
         assert call(n=3) == I and call(n=-1, cu=0x5000) == I and call(n=3, cu=0x5002) == I
         assert call(n=0, cu=0x5000) == OK and call(kv=_kv4(batch=0), n=0) == OK
+        assert call(n=0x7fff0001, cu=0x5000) == U
     assert append(ks=1023) == I and append(vs=1028) == I and append(ks=1016) == I and append(gate=0x5002) == I
     assert read(dtype=3) == I
 
