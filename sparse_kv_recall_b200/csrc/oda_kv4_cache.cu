@@ -1,19 +1,22 @@
 // Append rows to the 4-bit cache and read rows back ([ODA] 접근 방법: the fully retained history,
 // held in 144 bytes per position and KV head instead of 512).
 //
-// Bound: HBM bytes -- an appended row pair is 512 B read and 144 B written -- and close behind it
-// instruction issue (some 90 instructions a row pair and warp). A warp takes U (row, KV head) units: its
-// first U lanes look up where the units go, all at once, then for each unit the lanes hold 16 bytes of
-// the K row (0-15) and of the V row (16-31), so a group of 64 dims is 8 lanes and its ends three
-// shuffles. U = 8 where there are units enough to fill the GPU with such warps (the chain of dependent
-// loads that finds a slot is then paid once for eight units, and four rows are in flight); else U = 1.
+// Bound: HBM bytes -- an appended row pair is 512 B read and 144 B written, one read back the reverse -- and
+// for few rows the chain of dependent loads (ranges, length, page table, page) that finds a slot. A warp
+// takes eight (row, KV head) units where there are enough of them to give every SM such warps: its first eight
+// lanes look up where they go, all at once, and the rows of all eight are in flight together; else one unit.
+// Measured, bf16 in and out, eight units a warp / one (us):
+//   units       4,096        8,192        28,000       160,000
+//   append      3.6 / 3.4    4.3 / 4.1    6.5 / 9.4    24.4 / 46.6 (105 MB: 66 % of a copy's rate)
+//   read        3.2 / 3.0    3.3 / 3.6    4.9 / 7.7    19.8 / 39.7
 #include "oda_internal.h"
 #include "oda_kv4.cuh"
 
 namespace oda {
 
 constexpr int kRowWarps = 8;
-constexpr int kManyUnits = 8 * kRowWarps * 8 * 148;  // eight CTAs of U = 8 warps per SM
+constexpr int kMany = 8;                              // units a warp takes where there are many
+constexpr int kManyUnits = kMany * kRowWarps * 148;   // a CTA of such warps per SM
 
 struct RowsParams {
   unsigned char* cache;
@@ -95,90 +98,148 @@ struct Units {
 };
 
 // The rows are requested before their slots are looked up: neither needs the other.
+//
+// Eight units a warp: two at a time, 16 lanes each. Lane = 16 u + 8 isv + li holds dims 16 li .. 16 li + 15 of unit
+// u's K or V row: a group of 64 dims is then four lanes, its ends two shuffles, and what is done once per lane is
+// done for sixteen values.
 template <int U>
+__global__ void __launch_bounds__(kRowWarps * 32)
+    kv4_append_many_kernel(const RowsParams p, const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
+                           long long k_stride, long long v_stride) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, half = lane >> 4, isv = (lane >> 3) & 1, li = lane & 7;
+  Units<U> units(p, lane);
+  const __nv_bfloat16* base = (isv ? v_new : k_new) + 16 * li;
+  const long long stride = isv ? v_stride : k_stride;
+  uint4 v[U / 2][2];
+#pragma unroll
+  for (int u = 0; u < U / 2; ++u) {
+    const int i = units.row(2 * u + half), g = units.head(2 * u + half);
+    v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < p.num_rows) {
+      const uint4* src = reinterpret_cast<const uint4*>(base + i * stride + g * kHeadDim);
+      v[u][0] = src[0];
+      v[u][1] = src[1];
+    }
+  }
+  units.resolve(p, lane);
+  // words 4 (li % 4) + g and two further of group g = li / 4
+  const int word_off = isv * kKv4VOff + 16 * (li & 3) + 4 * (li >> 2);
+  const int meta_off = kKv4MetaOff + 8 * isv + 4 * (li >> 2);
+#pragma unroll
+  for (int u = 0; u < U / 2; ++u) {
+    const Slot s = units.at(2 * u + half);
+    uint32_t ends = bf2_max_nan(kv4_ends(v[u][0]), kv4_ends(v[u][1]));
+    ends = bf2_max_nan(ends, __shfl_xor_sync(0xffffffffu, ends, 1));
+    ends = bf2_max_nan(ends, __shfl_xor_sync(0xffffffffu, ends, 2));
+    const Kv4Group g = kv4_group(ends);
+    const uint32_t w0 = kv4_codes(v[u][0], g), w1 = kv4_codes(v[u][1], g);
+    if (s.row < 0) continue;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(s.page + word_off + s.row * kKv4RowBytes);
+    dst[0] = w0;
+    dst[2] = w1;
+    if ((li & 3) == 0) *reinterpret_cast<uint32_t*>(s.page + meta_off + s.row * kKv4MetaBytes) = g.meta;
+  }
+}
+
 __global__ void __launch_bounds__(kRowWarps * 32)
     kv4_append_kernel(const RowsParams p, const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
                       long long k_stride, long long v_stride) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  Units<U> units(p, lane);
-  const __nv_bfloat16* base = (lane < 16 ? k_new : v_new) + 8 * (lane & 15);
-  const long long stride = lane < 16 ? k_stride : v_stride;
-  uint4 v[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int i = units.row(u), g = units.head(u);
-    v[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (i < p.num_rows) v[u] = *reinterpret_cast<const uint4*>(base + i * stride + g * kHeadDim);
-  }
+  Units<1> units(p, lane);
+  const int i = units.row(0), g = units.head(0);
+  if (i >= p.num_rows) return;
+  const uint4 v = *reinterpret_cast<const uint4*>((lane < 16 ? k_new + i * k_stride : v_new + i * v_stride) +
+                                                  g * kHeadDim + 8 * (lane & 15));
   units.resolve(p, lane);
+  const Slot s = units.at(0);
+  if (s.row < 0) return;  // (uniform)
+  uint32_t meta;
+  const uint32_t word = kv4_quantise(v, lane, meta);
+  kv4_store_row(s.page, s.row, word, meta, lane);
+}
+
+// Eight values of a code word, minimum + c * scale, as four pairs.
+__device__ __forceinline__ void kv4_values(uint32_t w, uint32_t meta, float2 (&x)[4]) {
+  const float2 s = make_float2(kv4_scale(meta), kv4_scale(meta));
+  const float2 m = make_float2(kv4_min(meta), kv4_min(meta));
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const Slot s = units.at(u);
-    if (s.row < 0) continue;  // (uniform)
-    uint32_t meta;
-    const uint32_t word = kv4_quantise(v[u], lane, meta);
-    kv4_store_row(s.page, s.row, word, meta, lane);
+  for (int k = 0; k < 4; ++k) {  // a nibble in the mantissa of 2^23 is 2^23 + c
+    const uint32_t b = w >> (8 * k);
+    const float2 c = make_float2(__uint_as_float(0x4b000000u | (b & 15u)),
+                                 __uint_as_float(0x4b000000u | ((b >> 4) & 15u)));
+    x[k] = f2_fma2(f2_add(c, make_float2(-8388608.f, -8388608.f)), s, m);
   }
 }
 
-constexpr int kInFlight = 4;
+template <bool kBf16>
+__device__ __forceinline__ void kv4_write_values(void* out, size_t at, uint32_t w, uint32_t meta) {
+  float2 x[4];
+  kv4_values(w, meta, x);
+  if constexpr (kBf16) {
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[k].x, x[k].y);
+      o[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+    dst[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    dst[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+  }
+}
 
-template <int U, bool kBf16>
-__global__ void __launch_bounds__(kRowWarps * 32)
-    kv4_read_kernel(const RowsParams p, void* k_out, void* v_out) {
-  constexpr int N = U < kInFlight ? U : kInFlight;
+// One unit a warp: lane 16 isv + li reads dims 8 li .. + 7.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRowWarps * 32) kv4_read_kernel(const RowsParams p, void* k_out, void* v_out) {
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int li = lane & 15, isv = lane >> 4;
+  const int lane = threadIdx.x & 31, li = lane & 15, isv = lane >> 4;
+  Units<1> units(p, lane);
+  units.resolve(p, lane);
+  const Slot s = units.at(0);
+  if (s.row < 0) return;
+  const size_t at = ((size_t)units.row(0) * p.hkv + units.head(0)) * kHeadDim + 8 * li;
+  const uint32_t w =
+      *reinterpret_cast<const uint32_t*>(s.page + isv * kKv4VOff + s.row * kKv4RowBytes + 4 * kv4_word(li));
+  const uint32_t meta =
+      *reinterpret_cast<const uint32_t*>(s.page + kKv4MetaOff + s.row * kKv4MetaBytes + 4 * (lane >> 3));
+  kv4_write_values<kBf16>(isv ? v_out : k_out, at, w, meta);
+}
+
+// Two at a time: lane 16 u + 8 isv + li reads dims 8 li .. + 7 of both groups, words 2 li and 2 li + 1.
+template <int U, bool kBf16>
+__global__ void __launch_bounds__(kRowWarps * 32)
+    kv4_read_many_kernel(const RowsParams p, void* k_out, void* v_out) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, half = lane >> 4, isv = (lane >> 3) & 1, li = lane & 7;
   Units<U> units(p, lane);
   units.resolve(p, lane);
-  const int code_off = isv * kKv4VOff + 4 * kv4_word(li), meta_off = kKv4MetaOff + 4 * (lane >> 3);
+  const int code_off = isv * kKv4VOff + 8 * li, meta_off = kKv4MetaOff + 8 * isv;
+  void* out = isv ? v_out : k_out;
+  uint2 w[U / 2], meta[U / 2];
+  bool ok[U / 2];
 #pragma unroll
-  for (int u0 = 0; u0 < U; u0 += N) {
-    size_t at[N];
-    uint32_t w[N], meta[N];
-    bool ok[N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const Slot s = units.at(u0 + n);
-      ok[n] = s.row >= 0;
-      at[n] = ((size_t)units.row(u0 + n) * p.hkv + units.head(u0 + n)) * kHeadDim + 8 * li;
-      if (ok[n]) {
-        w[n] = *reinterpret_cast<const uint32_t*>(s.page + code_off + s.row * kKv4RowBytes);
-        meta[n] = *reinterpret_cast<const uint32_t*>(s.page + meta_off + s.row * kKv4MetaBytes);
-      }
+  for (int u = 0; u < U / 2; ++u) {
+    const Slot s = units.at(2 * u + half);
+    ok[u] = s.row >= 0;
+    if (ok[u]) {
+      w[u] = *reinterpret_cast<const uint2*>(s.page + code_off + s.row * kKv4RowBytes);
+      meta[u] = *reinterpret_cast<const uint2*>(s.page + meta_off + s.row * kKv4MetaBytes);
     }
+  }
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      if (!ok[n]) continue;
-      const float2 s = make_float2(kv4_scale(meta[n]), kv4_scale(meta[n]));
-      const float2 m = make_float2(kv4_min(meta[n]), kv4_min(meta[n]));
-      float2 x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {  // a nibble in the mantissa of 2^23 is 2^23 + c
-        const uint32_t b = w[n] >> (8 * k);
-        const float2 c = make_float2(__uint_as_float(0x4b000000u | (b & 15u)),
-                                     __uint_as_float(0x4b000000u | ((b >> 4) & 15u)));
-        x[k] = f2_fma2(f2_add(c, make_float2(-8388608.f, -8388608.f)), s, m);
-      }
-      if constexpr (kBf16) {
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(x[k].x, x[k].y);
-          o[k] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(isv ? v_out : k_out) + at[n]) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(isv ? v_out : k_out) + at[n]);
-        dst[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-        dst[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
-      }
-    }
+  for (int u = 0; u < U / 2; ++u) {
+    const size_t at = ((size_t)units.row(2 * u + half) * p.hkv + units.head(2 * u + half)) * kHeadDim + 8 * li;
+    if (!ok[u]) continue;
+    kv4_write_values<kBf16>(out, at, w[u].x, meta[u].x);
+    kv4_write_values<kBf16>(out, at + kKv4Group, w[u].y, meta[u].y);
   }
 }
 
@@ -218,7 +279,7 @@ static int rows_params(const oda_kv4* kv, int32_t num_rows, const int32_t* cu_ro
   if (num_rows > 0x7fff0000) return ODA_ERR_UNSUPPORTED_SHAPE;  // (the last warps' rows pass num_rows)
   const long long units = (long long)num_rows * kv->num_kv_heads;
   *many = units >= kManyUnits;
-  const long long per_cta = kRowWarps * (*many ? 8 : 1);
+  const long long per_cta = kRowWarps * (*many ? kMany : 1);
   const long long blocks = (units + per_cta - 1) / per_cta;
   if (blocks >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
   p->cache = static_cast<unsigned char*>(kv->cache);
@@ -256,7 +317,7 @@ extern "C" int oda_kv4_append(const oda_kv4* kv, const void* k_new, const void* 
       !aligned_or_null(v_new, 16))
     return ODA_ERR_INVALID_ARG;
   return cuda_status(launch_dependent(
-      many ? kv4_append_kernel<8> : kv4_append_kernel<1>, grid, kRowWarps * 32, 0,
+      many ? kv4_append_many_kernel<kMany> : kv4_append_kernel, grid, kRowWarps * 32, 0,
       static_cast<cudaStream_t>(stream), p, static_cast<const __nv_bfloat16*>(k_new),
       static_cast<const __nv_bfloat16*>(v_new), (long long)k_stride, (long long)v_stride));
 }
@@ -274,7 +335,8 @@ extern "C" int oda_kv4_read(const oda_kv4* kv, void* k_out, void* v_out, int32_t
       !aligned_or_null(v_out, 16))
     return ODA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const auto kernel = out_dtype == ODA_BF16 ? (many ? kv4_read_kernel<8, true> : kv4_read_kernel<1, true>)
-                                            : (many ? kv4_read_kernel<8, false> : kv4_read_kernel<1, false>);
+  const auto kernel = out_dtype == ODA_BF16
+                          ? (many ? kv4_read_many_kernel<kMany, true> : kv4_read_kernel<true>)
+                          : (many ? kv4_read_many_kernel<kMany, false> : kv4_read_kernel<false>);
   return cuda_status(launch_dependent(kernel, grid, kRowWarps * 32, 0, st, p, k_out, v_out));
 }

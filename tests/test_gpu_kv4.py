@@ -51,7 +51,7 @@ def test_append_and_read_of_many_rows_take_eight_at_a_time():
     such a group, one gated off."""
     lengths, hkv = [3000, 1, 17, 8192, 5, 250], 7
     n = sum(lengths)
-    assert n * hkv > 8 * 8 * 8 * 148 and n * hkv % 8 != 0
+    assert n * hkv > 8 * 8 * 148 and n * hkv % 8 != 0
     rows = [gauss((n, hkv, 128), 55 + i, 2.0) - i for i in range(2)]
     c = PagedCase(lengths, hkv, hkv, seed=57, rows=rows)
     k, v = _read_all(c)
@@ -135,6 +135,32 @@ def test_append_special_groups():
     assert np.array_equal(k.cpu().numpy(), ref.astype(np.float32), equal_nan=True)
     nan = np.isnan(ref[:, 0]).reshape(8, 2, 64).all(-1)
     assert nan.tolist() == [[False] * 2] * 4 + [[True, False], [False, True], [True, False], [False] * 2]
+
+
+@pytest.mark.parametrize("kind", range(6))
+def test_append_rounds_as_the_division_does(kind):
+    """Quotients at and beside halves: whole numbers and halves over spans of every kind, an offset, scales
+    down to the subnormal ones, by single rows and by eight at a time."""
+    for n in (40, 1500):
+        g = torch.Generator(device="cuda").manual_seed(200 + kind)
+        shape = (n, 8, 128)
+        x = torch.randint(0, 31, shape, generator=g, device="cuda").double() / 2
+        if kind == 1:
+            x = torch.randint(-40, 40, shape, generator=g, device="cuda").double()
+        if kind == 2:
+            x = torch.randint(0, 2000, shape, generator=g, device="cuda").double() / 64
+        if kind == 3:
+            x = x + 100
+        if kind >= 4:
+            x = torch.randn(shape, generator=g, device="cuda").double()
+            x = x * 2.0 ** torch.randint(*((-133, -90) if kind == 4 else (-90, 120)), (n, 8, 1), generator=g,
+                                         device="cuda").double()
+        rows = (x.to(torch.bfloat16), x.flip(0).to(torch.bfloat16))
+        c = PagedCase([n], 8, 8, seed=210, rows=rows)
+        k, v = _read_all(c)
+        for got, want in zip((k, v), rows):
+            ref = K.round_trip(want.double().cpu().numpy())
+            assert np.array_equal(got.cpu().numpy(), ref.astype(np.float32))
 
 
 def test_append_and_read_report_bad_sequences():
