@@ -6,14 +6,19 @@
 // (A launch runs most of this code once, so loops of few trips are not unrolled: the instruction cache is cold.)
 //
 // One thread-block cluster takes one (sequence, KV head). The threshold weight is found by a radix select
-// over order-preserving 32-bit keys, eight bits a pass from the highest bit in which any two keys differ;
-// every later decision follows from it and from
+// over order-preserving 32-bit keys, eight bits a pass from the highest bit in which any two keys differ,
+// until few keys are left that are compared with one another; every later decision follows from it and from
 // counts, so the result does not depend on any order of execution. Up to kAlone slots every CTA of the
 // cluster selects by itself, from all the keys, and moves its share of the rows: a pass is then two CTA
 // barriers, where histograms summed through distributed shared memory cost a cluster barrier and a remote
-// read (2304 slots, budget 2048, one sequence of 8 KV heads: 22.9 us with shared histograms, 13.0 so). Longer sequences are shared out over the cluster. Bound: memory -- a kept row is
-// read and written once (512 bytes in bf16, 144 in 4 bits), a weight is read a few times, mostly out of
-// L2 or shared memory.
+// read (2304 slots, budget 2048, one sequence of 8 KV heads: 22.9 us with shared histograms, 13.3 so).
+// Longer sequences are shared out over the cluster.
+//
+// Bound: memory for the rows -- a kept row is read and written once (512 bytes in bf16, 144 in 4 bits), a
+// weight is read a few times, mostly out of L2 or shared memory -- and before them, not overlapped, the
+// selection's chain of barriers and scans. Four sequences of 20K to 32K cut down to 4096 (135 MB of bf16 rows):
+// 44.5 us, of which the move takes 19, at the rate of a copy, and the selection 20; 16 sequences of 1.5K to
+// 8K in 4 bits down to 2049: 37.7 us, 13 of them the move.
 //
 // In place, a move must not overwrite a row that has not been read. The i-th kept slot p_i is >= i,
 // so when the rows of a round, a run [i0, i1) of the kept list, are all in registers before the
@@ -103,14 +108,18 @@ __device__ __forceinline__ unsigned warp_scan(unsigned v, int lane) {  // inclus
 constexpr int kKeyCache = 8192;    // keys held in shared memory: all of a sequence's up to as many slots
 constexpr int kAlone = kKeyCache;  // (each CTA then selects by itself), else a CTA's share (more: read again)
 
-constexpr int kFew = 128;
+constexpr int kFew = 128;     // keys that are compared with one another directly, by four threads each
+constexpr int kAhead = 6;     // weights a thread has in flight (2304 slots: 13.3 us with 4 or 6, 13.9 with 8;
+                              // 8K in 4 bits, 16 sequences: 38.1 with 4, 37.7 with 6, 37.1 with 8)
+static_assert(kFew * 4 == kEvictThreads, "a thread per key and part of the comparisons");
 
 struct EvictSmem {
   unsigned keys[kKeyCache];
   uint16_t list[kAlone];      // alone: the kept slots
   unsigned hist[2][256];
   unsigned bad, in_place, digit, need, here, kmin, kmax, threshold;
-  unsigned few[kFew], nfew;   // keys of the digit that holds the threshold, once they are few
+  unsigned few[kFew], nfew;   // keys of the digit that holds the threshold, once they are few ...
+  unsigned all[kFew], above;  // ... the cluster's, in rank order; this CTA's slots that stay above that digit
   unsigned wmin[kEvictWarps], wmax[kEvictWarps];
   unsigned gt[kEvictWarps], eq[kEvictWarps], total[2];
   unsigned src[2][kEvictThreads], dst[2][kEvictThreads];  // rows of two rounds, as page * 16 + row
@@ -159,32 +168,45 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
   };
 
   // ---- page checks, keys and the range they span ----
-  if (tid == 0) s.bad = s.nfew = 0u;
+  if (tid == 0) s.bad = s.nfew = s.above = 0u;
   for (int i = tid; i < 512; i += kEvictThreads) s.hist[i >> 8][i & 255] = 0u;
   __syncthreads();
+  unsigned kmin = 0xffffffffu, kmax = 0u;
   if (usable) {
+    // (the first pages' ids are on their way beside the weights)
     const int src_pages = (len + kPage - 1) / kPage, dst_pages = (keep + kPage - 1) / kPage;
+    int i = part * kEvictThreads + tid;
+    int src = i < src_pages ? table[i] : 0, dst = i < dst_pages ? dst_table[i] : -1;
+    if (select) {
+#pragma unroll 1
+      for (int base = my_lo + tid; base < my_hi; base += kAhead * kEvictThreads) {
+        float m[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (base + u * kEvictThreads < my_hi) m[u] = mass[base + u * kEvictThreads];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (base + u * kEvictThreads >= my_hi) break;
+          const unsigned k = mass_key(m[u]);
+          if (cached) s.keys[base + u * kEvictThreads - lo] = k;
+          kmin = min(kmin, k);
+          kmax = max(kmax, k);
+        }
+      }
+    }
     bool bad = false, same = false;  // (a destination table may be a copy of the source's)
 #pragma unroll 1
-    for (int i = part * kEvictThreads + tid; i < src_pages; i += parts * kEvictThreads)
-      bad |= (unsigned)table[i] >= (unsigned)p.num_blocks;
-#pragma unroll 1
-    for (int i = part * kEvictThreads + tid; i < dst_pages; i += parts * kEvictThreads) {
-      bad |= (unsigned)dst_table[i] >= (unsigned)p.num_blocks;
-      same |= dst_table[i] == table[i];
+    while (i < src_pages) {
+      bad |= (unsigned)src >= (unsigned)p.num_blocks || (i < dst_pages && (unsigned)dst >= (unsigned)p.num_blocks);
+      same |= dst == src;
+      i += parts * kEvictThreads;
+      if (i < src_pages) src = table[i];
+      dst = i < dst_pages ? dst_table[i] : -1;
     }
     if (bad) atomicOr(&s.bad, 1u);
     if (same) atomicOr(&s.bad, 2u);
   }
-  unsigned kmin = 0xffffffffu, kmax = 0u;
   if (select) {
-#pragma unroll 4
-    for (int i = my_lo + tid; i < my_hi; i += kEvictThreads) {
-      const unsigned k = mass_key(mass[i]);
-      if (cached) s.keys[i - lo] = k;
-      kmin = min(kmin, k);
-      kmax = max(kmax, k);
-    }
     warp_range(kmin, kmax);
     if (lane == 0) {
       s.wmin[warp] = kmin;
@@ -228,16 +250,18 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
       p.ticket[b] = 0u;
       p.lens_out[b] = skip ? len : keep;
     }
-    if (!alone) cluster_sync();  // nobody leaves while its shared memory may still be read
   };
   if (skip) {
     leave();
+    if (!alone) cluster_sync();  // nobody leaves while its shared memory may still be read
     return;
   }
 
   if (select) {
     unsigned need = p.budget - p.sink - p.recent;  // keys above the threshold stay, `need` of its equals
     unsigned threshold = 0xffffffffu;
+    bool located = false;  // not alone: gt_before, eq_before count the CTAs before this one
+    unsigned gt_before = 0u, eq_before = 0u;
     if (need > 0 && kmin == kmax) {
       threshold = kmin;
     } else if (need > 0) {
@@ -300,44 +324,65 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
         if (s.here > kFew) continue;
         // Few enough to be compared with one another: the threshold is the one with fewer than `need` keys
         // above it and at least as many not below it.
+        unsigned over = 0u;
 #pragma unroll 1
         for (int i = my_lo + tid; i < my_hi; i += kEvictThreads) {
-          const unsigned k = key(i);
-          if ((k >> shift) == prefix) s.few[atomicAdd(&s.nfew, 1u)] = k;
+          const unsigned k = key(i) >> shift;
+          if (k == prefix) s.few[atomicAdd(&s.nfew, 1u)] = key(i);
+          over += k > prefix;
+        }
+        if (!alone) {
+          over = warp_scan(over, lane);
+          if (lane == 31 && over) atomicAdd(&s.above, over);
         }
         __syncthreads();
-        unsigned mine = 0u;
-        int few = 0;
+        int few = 0, few_before = 0;
         if (alone) {
           few = (int)s.nfew;
-          if (tid < few) mine = s.few[tid];
+          if (tid < few) s.all[tid] = s.few[tid];
         } else if constexpr (C > 1) {
+          // every slot of this CTA that is kept in any case, and the keys above the digit
+          if (tid == 0) s.above += (unsigned)(hi - lo - max(0, my_hi - my_lo));
           cluster_sync();
+          unsigned mine = 0u;
 #pragma unroll
           for (int r = 0; r < C; ++r) {  // thread t: the cluster's t-th
             const int nr = (int)dsmem_ld_u32(&s.nfew, r);
+            const unsigned ar = dsmem_ld_u32(&s.above, r);
             if (tid >= few && tid < few + nr) mine = dsmem_ld_u32(&s.few[tid - few], r);
             few += nr;
+            few_before += r < (int)rank ? nr : 0;
+            gt_before += r < (int)rank ? ar : 0u;
           }
-          cluster_sync();  // everyone has everyone's
-          if (tid < few) s.few[tid] = mine;
-          __syncthreads();
+          if (tid < few) s.all[tid] = mine;
         }
-        if (tid < few) {
-          unsigned above = 0u, same = 0u;
+        __syncthreads();
+        const unsigned mine = s.all[tid >> 2];  // (few <= kFew; what lies behind is not looked at)
+        unsigned above = 0u, same = 0u;
 #pragma unroll 4
-          for (int j = 0; j < few; ++j) {
-            above += s.few[j] > mine;
-            same += s.few[j] == mine;
-          }
-          if (above < need && above + same >= need) {  // (threads of equal keys write the same)
-            s.threshold = mine;
-            s.need = need - above;
-          }
+        for (int j = tid & 3; j < few; j += 4) {
+          const unsigned other = s.all[j];
+          above += other > mine;
+          same += other == mine;
+        }
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          above += __shfl_xor_sync(0xffffffffu, above, o);
+          same += __shfl_xor_sync(0xffffffffu, same, o);
+        }
+        if ((tid >> 2) < few && above < need && above + same >= need) {  // (threads of equal keys write the same)
+          s.threshold = mine;
+          s.need = need - above;
         }
         __syncthreads();
         threshold = s.threshold;
         need = s.need;
+        if (!alone) {
+          const unsigned theirs = tid < few_before ? s.all[tid] : 0u;
+          gt_before += (unsigned)__syncthreads_count(tid < few_before && theirs > threshold);
+          eq_before = (unsigned)__syncthreads_count(tid < few_before && theirs == threshold);
+          located = true;
+        }
         break;
       }
     }
@@ -365,20 +410,20 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
       eq += e;
     }
     // scans over the warp, then the warps before
-    unsigned gt_before = warp_scan(gt, lane), eq_before = warp_scan(eq, lane);
+    const unsigned gt_upto = warp_scan(gt, lane), eq_upto = warp_scan(eq, lane);
     if (lane == 31) {
-      s.gt[warp] = gt_before;
-      s.eq[warp] = eq_before;
+      s.gt[warp] = gt_upto;
+      s.eq[warp] = eq_upto;
     }
-    gt_before -= gt;
-    eq_before -= eq;
+    gt_before += gt_upto - gt;
+    eq_before += eq_upto - eq;
     __syncthreads();
 #pragma unroll 1
     for (int w = 0; w < warp; ++w) {
       gt_before += s.gt[w];
       eq_before += s.eq[w];
     }
-    if (!alone) {
+    if (!alone && !located) {
       if (tid == kEvictThreads - 1) {
         s.total[0] = gt_before + gt;
         s.total[1] = eq_before + eq;
@@ -461,6 +506,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const EvictPara
 #pragma unroll 1
   for (int i = keep + rank * kEvictThreads + tid; i < len; i += C * kEvictThreads) mass_out[i] = 0.f;
   leave();
+  // Nothing is read from the other CTAs any more, but a cluster whose CTAs leave together makes room for the next
+  // launch's at once (sequences of 20K to 32K, calls one behind the other: 44.3 us, 47 without).
+  if (!alone) cluster_sync();
 }
 
 // CTAs per cluster: as many (at most 16) as keep all clusters within two waves of one CTA per SM,
