@@ -1,7 +1,7 @@
 // The 4-bit KV page and the row quantiser shared by the kernels that write and read it.
 //
-// One (page, KV head) is one contiguous run of 2304 bytes, so that a decode warp brings it in
-// with a single bulk copy: K codes [16 tokens][64 B], V codes [16][64 B], meta [16][4 words].
+// One (page, KV head) is one contiguous run of 2304 bytes, 144 16-byte pieces, so that a decode warp brings
+// two of them in with nine copies a lane: K codes [16 tokens][64 B], V codes [16][64 B], meta [16][4 words].
 // A row's 128 dims are two groups of 64, each with its own scale s and minimum m; a code c in
 // 0..15 stands for m + c s. Word 2 i + g of a row's 16 words holds dims 64 g + 8 i .. + 7 of
 // group g in its nibbles, lowest first; the meta words of a token are (K g0, K g1, V g0, V g1),

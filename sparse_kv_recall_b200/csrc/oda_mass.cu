@@ -5,8 +5,10 @@
 // when the decode kernel's last merge is done. So the decode kernel leaves every visible position's
 // score in the workspace (4 bytes a query head, where recomputing it would read the K row again:
 // 256 bytes in bf16, 72 in 4 bits) and a second kernel, launched with a programmatic dependency,
-// turns scores into weights and adds them up over the query heads of the KV head. Bound: memory,
-// 4 G + 8 bytes per position and KV head, the scores mostly out of L2.
+// turns scores into weights and adds them up over the query heads of the KV head. Bound: latency (length,
+// page and scores, then the weights' store) and memory, 4 G + 8 bytes per position and KV head, the scores
+// mostly out of L2. Two sequences of 32,769 tokens, 8 KV heads, 32 query heads: 59.9 us in all, 53.4 of them the
+// bf16 attention by itself; eight of 9K to 16K in 4 bits, 16 query heads: 38.4, of them 32.6.
 #include <math.h>
 
 #include "oda_decode.cuh"
