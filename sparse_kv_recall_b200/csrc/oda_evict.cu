@@ -18,7 +18,8 @@
 // weight is read a few times, mostly out of L2 or shared memory -- and before them, not overlapped, the
 // selection's chain of barriers and scans. Four sequences of 20K to 32K cut down to 4096 (135 MB of bf16 rows):
 // 44.5 us, of which the move takes 19, at the rate of a copy, and the selection 20; 16 sequences of 1.5K to
-// 8K in 4 bits down to 2049: 37.7 us, 13 of them the move.
+// 8K in 4 bits down to 2049: 35.7 us, 13 of them the move. (Fetching the recent rows, which move in any case,
+// into L2 beside the selection: 48.5 us for the former.)
 //
 // In place, a move must not overwrite a row that has not been read. The i-th kept slot p_i is >= i,
 // so when the rows of a round, a run [i0, i1) of the kept list, are all in registers before the
@@ -105,8 +106,9 @@ __device__ __forceinline__ unsigned warp_scan(unsigned v, int lane) {  // inclus
   return v;
 }
 
-constexpr int kKeyCache = 8192;    // keys held in shared memory: all of a sequence's up to as many slots
-constexpr int kAlone = kKeyCache;  // (each CTA then selects by itself), else a CTA's share (more: read again)
+constexpr int kKeyCache = 8192;  // keys held in shared memory (a CTA's share of more is read again)
+constexpr int kAlone = 4096;     // slots up to which each CTA of a cluster selects by itself (2304: 13.3 us,
+                                 // shared 23.1; 8K in 4 bits, two CTAs a cluster: 37.4 us, shared 35.7)
 
 constexpr int kFew = 128;     // keys that are compared with one another directly, by four threads each
 constexpr int kAhead = 6;     // weights a thread has in flight (2304 slots: 13.3 us with 4 or 6, 13.9 with 8;
@@ -115,7 +117,7 @@ static_assert(kFew * 4 == kEvictThreads, "a thread per key and part of the compa
 
 struct EvictSmem {
   unsigned keys[kKeyCache];
-  uint16_t list[kAlone];      // alone: the kept slots
+  uint16_t list[kKeyCache];   // alone and cached: the kept slots
   unsigned hist[2][256];
   unsigned bad, in_place, digit, need, here, kmin, kmax, threshold;
   unsigned few[kFew], nfew;   // keys of the digit that holds the threshold, once they are few ...

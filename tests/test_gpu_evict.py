@@ -210,6 +210,18 @@ def test_evict_matches_oracle(kv4, ties, lens, hkv, sink, recent, budget, in_pla
 
 
 @BOTH
+def test_evict_many_heads_of_many_slots(kv4):
+    """Too many (sequence, KV head)s for more than one CTA each, and more than 4096 slots kept of some."""
+    lens = [8192, 7001] + [30 + i for i in range(17)]
+    c = PagedCase(lens, 8, 8, seed=131, kv4=kv4)
+    mass = _random_mass(c, 132)
+    old, old_mass = (c.k.copy(), c.v.copy()), mass.clone()
+    kept, mass_out, new_lens = _evict(c, mass, 4, 300, 6500)
+    c.ok()
+    _assert_evicted(c, lens, c.bt, old, old_mass, kept, mass_out, new_lens, 4, 300, 6500)
+
+
+@BOTH
 def test_evict_orders_every_kind_of_weight(kv4):
     """Equal weights, zeros of both signs, infinities, subnormals and negative numbers."""
     c = PagedCase([64], 1, 1, seed=130, kv4=kv4)
