@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
     }
     if (n_contrib > 1) {
       __syncthreads();  // the CTA's partial is written; thread 0 publishes it (release)
-      if (tid == 0) s_last = ticket_arrive(&p.ws_ticket[bg]) == (unsigned)(n_contrib - 1);
+      if (tid == 0) s_last = ticket_arrive(&p.ws_ticket[piece.first]) == (unsigned)(n_contrib - 1);
       __syncthreads();  // ... and the last CTA's thread 0 acquired everyone's partials
       if (s_last) {
         // The partials come into shared memory by asynchronous copies, as many at a time as the stages
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
           kv4_write(p, b, g * G + h, e % kHeadDim, none ? 0.f : a[k] / s_sum[h],
                     none ? -INFINITY : s_max[h] + log2f(s_sum[h]));
         }
-        if (tid == 0) p.ws_ticket[bg] = 0u;  // leave the workspace zeroed
+        if (tid == 0) p.ws_ticket[piece.first] = 0u;  // leave the tickets zeroed
       }
     }
     x = piece.x_end;
@@ -826,16 +826,19 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
 // ---------------------------------------------------------------------------------------
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Tickets, then partials and their log-sums. A ticket belongs to the CTA a shared (sequence, KV head) begins in
+// (only the last one that begins in a CTA reaches past it): as many as CTAs and in front, so that they lie in
+// the same place for every batch and head count and one workspace serves calls of any.
 struct Kv4Ws {
-  size_t lse_off, ticket_off, total;
+  size_t o_off, lse_off, total;
 };
 
 static Kv4Ws kv4_ws(int batch, int hkv, int G, int sms) {
   const size_t slots = (size_t)sms * kCtasPerSm4 + (size_t)batch * hkv;
   Kv4Ws w;
-  w.lse_off = up256(slots * G * kHeadDim * sizeof(float));
-  w.ticket_off = w.lse_off + up256(slots * G * sizeof(float));
-  w.total = w.ticket_off + up256((size_t)batch * hkv * sizeof(unsigned));
+  w.o_off = up256((size_t)sms * kCtasPerSm4 * sizeof(unsigned));
+  w.lse_off = w.o_off + up256(slots * G * kHeadDim * sizeof(float));
+  w.total = w.lse_off + up256(slots * G * sizeof(float));
   return w;
 }
 
@@ -897,9 +900,9 @@ int launch_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* 
   p.scores = scores;
   p.cap = cap;
   unsigned char* w = static_cast<unsigned char*>(ws);
-  p.ws_o = reinterpret_cast<float*>(w);
+  p.ws_o = reinterpret_cast<float*>(w + wl.o_off);
   p.ws_lse = reinterpret_cast<float*>(w + wl.lse_off);
-  p.ws_ticket = reinterpret_cast<unsigned*>(w + wl.ticket_off);
+  p.ws_ticket = reinterpret_cast<unsigned*>(w);
   p.status = kv->dev_status;
   p.stats = kv->stats;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -493,3 +493,31 @@ def test_one_sequence_of_many_ctas_for_each_head_count():
         ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t))
         assert_out_close(out, ref, "G %d hkv %d" % (G, hkv))
         assert_lse_close(lse.cpu().numpy(), rlse)
+
+
+def test_one_workspace_for_calls_of_every_shape():
+    """Batches, head counts and lengths in turn over one workspace, the attention alone and with weights;
+    (sequence, KV head)s that begin and end inside a CTA's share among them."""
+    cases = [PagedCase([9000], 4, 1, seed=300), PagedCase([700, 3, 2100, 44], 16, 4, seed=301),
+             PagedCase([3000 + 17 * i for i in range(24)], 8, 8, seed=302), PagedCase([6000, 12000], 6, 3, seed=303)]
+    refs = []
+    for c in cases:
+        refs.append((c.out(), c.out(), torch.zeros((c.B, c.hkv, c.maxb * 16), device="cuda")))
+        (o, l), (o2, l2), m = refs[-1]
+        oda.oda_kv4_decode(c.kv, full(), c.q, SCALE, o, c.ws, lse=l)
+        oda.oda_kv4_decode_mass(c.kv, full(), c.q, SCALE, o2, torch.zeros_like(c.ws), m, lse=l2)
+        c.ok()
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+    ref, rlse, _ = cases[2].oracle(lambda b, t: O.full_positions(t))
+    assert_out_close(refs[2][0][0], ref)
+    ws = torch.zeros(max(c.ws.numel() for c in cases), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 3, 2, 0, 3, 1, 1, 2, 0):
+        c, ((o, l), _, m) = cases[i], refs[i]
+        out, lse = c.out()
+        oda.oda_kv4_decode(c.kv, full(), c.q, SCALE, out, ws, lse=lse)
+        out2, lse2 = c.out()
+        got = torch.zeros_like(m)
+        oda.oda_kv4_decode_mass(c.kv, full(), c.q, SCALE, out2, ws, got, lse=lse2)
+        c.ok()
+        assert torch.equal(out, o) and torch.equal(lse, l), i
+        assert torch.equal(out2, o) and torch.equal(lse2, l) and torch.equal(got, m), i
