@@ -757,10 +757,15 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
         __syncthreads();
         if (warp < G) {
           float m = -INFINITY, sum = 0.f;
+          bool any = false;  // some log-sum is not -inf: a number, or a NaN, which a maximum passes over
 #pragma unroll 1
-          for (int s = lane; s < n_contrib; s += 32) m = fmaxf(m, sw[s * G + warp]);
+          for (int s = lane; s < n_contrib; s += 32) {
+            m = fmaxf(m, sw[s * G + warp]);
+            any |= sw[s * G + warp] != -INFINITY;
+          }
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (__any_sync(0xffffffffu, any) && m == -INFINITY) m = 0.f;  // (NaNs alone: the weights are NaN)
 #pragma unroll 1
           for (int s = lane; s < n_contrib; s += 32) {
             const float ls = sw[s * G + warp];
