@@ -17,8 +17,9 @@
 //       A = codes as dims x 16 tokens, B = w_p S_g as a sum of two fp16 (columns (head, part): 22
 //       bits); the second sum has one term per token and group and runs on the CUDA cores. The codes
 //       are centred, z_p = 8 and 7 in turn (7.5 on average): over a long history an offset would grow
-//       with the token count and the signal only with its square root. w S enters by a running power
-//       of two per head and group that is raised when a weight passes 2^15.
+//       with the token count and the signal only with its square root. w S enters times a running power
+//       of two per head and group, r: lowered when a product passes 2^15 (to below 2^8), and raised with
+//       the softmax maximum by what the earlier weights lose.
 //
 // A code becomes an fp16 by an and-or that puts its nibble into the mantissa of 1024 and one exact
 // fp16 add or fma that takes the offset off.
@@ -134,7 +135,11 @@ struct Kv4State {
   float acc[8][4];     // tile 4 g + j: dims 64 g + 8 gid + j (0, 1) and + j + 4 (2, 3); columns
 };                     // 2 tig, 2 tig + 1 are the two parts of the head
 
-constexpr float kR0 = 1.2676506e30f;   // 2^100
+constexpr int kRTop = 253;             // exponent field of r at its largest, 2^126
+// A power of two by its exponent field, and the field of a number >= 0.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)e << 23); }
+__device__ __forceinline__ int pow2_exp(float x) { return (int)(__float_as_uint(x) >> 23); }
+
 constexpr float kNoMax = -1e30f;       // running maximum before any visible score
 
 // The group's q as B fragments (scaled to q') and, for the lane's own head, sum q' of each group and the
@@ -303,15 +308,22 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
   if (__any_sync(0xffffffffu, top > st.m + kLazyMax)) {
     const float mx = over_head(top);
     const bool up = mx > st.m + kLazyMax;
-    const float al = up ? ex2_fast(st.m - mx) : 1.f;
+    const float d = up ? mx - st.m : 0.f, al = ex2_fast(-d);
     if (up) st.m = mx;
     st.l *= al;
-    st.corr[0] *= al;
-    st.corr[1] *= al;
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int g = 0; g < 2; ++g) {
+      st.corr[g] *= al;
+      // What the weights so far lose, r gets back, to 2^126: it belongs to the weights that count now, and a
+      // row with a large scale that has become negligible does not leave the others below the fp16 range.
+      const float back = fminf(floorf(d), (float)(kRTop - pow2_exp(st.r[g])));
+      const float left = ex2_fast(back - d);  // al times that power of two
+      st.r[g] = pow2(pow2_exp(st.r[g]) + (int)back);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st.acc[t][i] *= al;
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.acc[4 * g + j][i] *= left;
+    }
   }
 
   // ---- weights times the V scales ----
@@ -340,16 +352,14 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const float ym = over_head(ymax[g]);
-      float ratio = 1.f;
-      if (ym * st.r[g] > 32768.f) {  // the largest weight to [2^7, 2^8)
-        const float rn = __uint_as_float((261u - min(__float_as_uint(ym) >> 23, 254u)) << 23);
-        ratio = rn / st.r[g];
-        st.r[g] = rn;
-      }
+      const int was = pow2_exp(st.r[g]);  // the largest weight to [2^7, 2^8)
+      const int e = ym * st.r[g] > 32768.f ? 261 - min(pow2_exp(ym), 254) : was;
+      const float less = pow2(max(0, 127 + e - was));
+      st.r[g] = pow2(e);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st.acc[4 * g + j][i] *= ratio;
+        for (int i = 0; i < 4; ++i) st.acc[4 * g + j][i] *= less;
     }
   }
   // as two fp16 each
@@ -624,7 +634,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
     st.m = kNoMax;
     st.l = 0.f;
     st.corr[0] = st.corr[1] = 0.f;
-    st.r[0] = st.r[1] = kR0;
+    st.r[0] = st.r[1] = pow2(kRTop);
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -691,7 +701,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
       if (tig < HG) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float inv = 1.f / st.r[i];
+          const float inv = pow2(254 - pow2_exp(st.r[i]));
           float o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {

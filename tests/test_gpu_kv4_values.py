@@ -1,14 +1,20 @@
 """Values at the ends of their ranges in decode over the 4-bit cache: a NaN that has to show however the
-history is shared out. Tolerances are those of kv4_cases."""
+history is shared out, V scales and scores that change along a warp's pages.
+
+Tolerances are those of kv4_cases: a weight is off by a few ulp of its score, so where scores reach 8 times
+those of the other tests (128 in base 2) so does the bound, WIDE; outputs are measured against the range of
+the V rows that carry the weight."""
+import numpy as np
 import pytest
 import torch
 
-from kv4_cases import SCALE, PagedCase, assert_lse_close, assert_out_close, full, gauss
+from kv4_cases import MAX, SCALE, PagedCase, assert_lse_close, assert_out_close, full, gauss
 from oracle import oda_oracle as O
 from sparse_kv_recall_b200 import build as B
 from sparse_kv_recall_b200 import oda
 
 pytestmark = pytest.mark.gpu
+WIDE = 8
 GROUPS = pytest.mark.parametrize("G", [1, 2, 4])
 
 
@@ -46,3 +52,36 @@ def test_a_nan_in_k_shows_however_many_ctas_share_the_history(rows):
     c = PagedCase([n], 2, 1, seed=412, rows=kv)
     out, lse = _decode(c)
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+def _share_pages(c, times):
+    """`times` sequences of other queries over the pages of c's one: many steps a warp."""
+    c.B, c.lengths = times, c.lengths * times
+    c.bt = c.bt.expand(times, -1).contiguous()
+    c.seq_lens = c.seq_lens.expand(times).contiguous()
+    c.bt_h = c.bt.cpu().numpy()
+    c.q = gauss((times, c.hq, 128), 423)
+    c.kv = oda.make_kv4(c.cache, c.bt, c.seq_lens, c.status, c.stats)
+    c.ws = torch.zeros(oda.oda_kv4_decode_workspace_size(times, c.hkv, c.hq), dtype=torch.uint8, device="cuda")
+
+
+@GROUPS
+@pytest.mark.parametrize("times", [1, 12])
+@pytest.mark.parametrize("k", [0, 28, 40, 60])
+def test_v_rows_that_lost_their_weight_leave_the_others_exact(G, times, k):
+    """Runs of 256 positions in turn (a warp's successive steps are 256 apart): V rows 2^k times as large at scores
+    91.8 lower in base 2, then ordinary rows. What the former add is at most 5 x 2^(60 - 91.8); the latter
+    have to come out as if they were alone. With 12 sequences a warp takes four steps and more."""
+    n, hkv = 12000, 2
+    kk, vv = gauss((n, hkv, 128), 420).float(), gauss((n, hkv, 128), 421).float()
+    low = (torch.arange(n, device="cuda") // 256 % 2 == 0).view(-1, 1)
+    kk[..., 0] = torch.where(low, 0.0, 45.0)
+    vv *= torch.where(low, 2.0 ** k, 1.0)[..., None]
+    c = PagedCase([n], G * hkv, hkv, seed=422, rows=(kk.to(torch.bfloat16), vv.to(torch.bfloat16)))
+    if times > 1:
+        _share_pages(c, times)
+    c.q[..., 0] = 16.0
+    out, lse = _decode(c)
+    ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t))
+    assert np.abs(out.double().cpu().numpy() - ref).max() <= MAX * WIDE
+    assert np.abs(lse.double().cpu().numpy() - rlse).max() <= 1e-4 * WIDE
