@@ -12,7 +12,8 @@
 //       mma.sync m16n8k16 fp16, A = 16 tokens x codes, B = columns (head, group) that hold the head's q
 //       in the dims of their group and zero elsewhere. q is scaled by a power of two to the top of the
 //       fp16 range: its eight significant bits fit, so every dim within 2^-28 of the head's largest is
-//       exact.
+//       exact. The codes enter times 2^-14, exact too: scales and minima up to 2^117 leave fp32's range
+//       only where the score does.
 //   V:  o_d = sum_p (w_p S_g) (c - z_p) + sum_p w_p (M_g + z_p S_g)
 //       A = codes as dims x 16 tokens, B = w_p S_g as a sum of two fp16 (columns (head, part): 22
 //       bits); the second sum has one term per token and group and runs on the CUDA cores. The codes
@@ -101,18 +102,28 @@ __device__ __forceinline__ float2 h2_unpack(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// The four nibbles of each half of w as fp16 pairs c - Z (Z = 8 or 7): even ones sit in bits 0-3,
-// odd ones in bits 4-7 of each half of w or of w >> 8.
-template <int Z>
+// The four nibbles of each half of w as fp16 pairs c - Z (Z = 8 or 7), times 2^-14 with kDown: even ones sit in
+// bits 0-3, odd ones in bits 4-7 of each half of w or of w >> 8.
+template <int Z, bool kDown = false>
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&a)[4]) {
   constexpr uint32_t kBase = 0x64006400u;                             // 1024
-  constexpr uint32_t kEven = Z == 8 ? 0xe408e408u : 0xe407e407u;      // - (1024 + Z)
-  constexpr uint32_t kOdd = Z == 8 ? 0xd480d480u : 0xd470d470u;       // - (64 + Z), after / 16
   const uint32_t w8 = w >> 8;
-  a[0] = h2_add(and_or(w, 0x000f000fu, kBase), kEven);
-  a[1] = h2_fma(and_or(w, 0x00f000f0u, kBase), 0x2c002c00u, kOdd);
-  a[2] = h2_add(and_or(w8, 0x000f000fu, kBase), kEven);
-  a[3] = h2_fma(and_or(w8, 0x00f000f0u, kBase), 0x2c002c00u, kOdd);
+  if constexpr (kDown) {
+    static_assert(Z == 8, "the constants are for 8");
+    constexpr uint32_t kEven = 0x04000400u, kOdd = 0x00400040u;       // 2^-14, 2^-18
+    constexpr uint32_t kEvenZ = 0xac08ac08u, kOddZ = 0x9c809c80u;     // - 1032 x 2^-14, - 72 x 2^-14
+    a[0] = h2_fma(and_or(w, 0x000f000fu, kBase), kEven, kEvenZ);
+    a[1] = h2_fma(and_or(w, 0x00f000f0u, kBase), kOdd, kOddZ);
+    a[2] = h2_fma(and_or(w8, 0x000f000fu, kBase), kEven, kEvenZ);
+    a[3] = h2_fma(and_or(w8, 0x00f000f0u, kBase), kOdd, kOddZ);
+  } else {
+    constexpr uint32_t kEven = Z == 8 ? 0xe408e408u : 0xe407e407u;    // - (1024 + Z)
+    constexpr uint32_t kOdd = Z == 8 ? 0xd480d480u : 0xd470d470u;     // - (64 + Z), after / 16
+    a[0] = h2_add(and_or(w, 0x000f000fu, kBase), kEven);
+    a[1] = h2_fma(and_or(w, 0x00f000f0u, kBase), 0x2c002c00u, kOdd);
+    a[2] = h2_add(and_or(w8, 0x000f000fu, kBase), kEven);
+    a[3] = h2_fma(and_or(w8, 0x00f000f0u, kBase), 0x2c002c00u, kOdd);
+  }
 }
 
 // Lane roles. gid = lane / 4, tig = lane % 4. A step takes two pages. The accumulator columns are
@@ -140,10 +151,10 @@ constexpr int kRTop = 253;             // exponent field of r at its largest, 2^
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)e << 23); }
 __device__ __forceinline__ int pow2_exp(float x) { return (int)(__float_as_uint(x) >> 23); }
 
-constexpr float kNoMax = -1e30f;       // running maximum before any visible score
+constexpr float kNoMax = -3.4028234e38f;  // running maximum before any visible score: below every other
 
-// The group's q as B fragments (scaled to q') and, for the lane's own head, sum q' of each group and the
-// factor that undoes q's power of two. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
+// The group's q as B fragments (scaled to q') and, for the lane's own head, 2^-14 sum q' of each group and the
+// factor that undoes q's power of two and the codes' 2^-14. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
 // word e = s / 2 of the lane's 16-byte code chunk, which is all group e & 1.
 template <int G>
 __device__ __forceinline__ void load_q4(const __nv_bfloat16* q, int lane, uint4 (&v)[4]) {
@@ -187,9 +198,9 @@ __device__ __forceinline__ float prepare_q4(const uint4 (&v)[4], int lane, uint3
     b[s][1] = mine ? h2_pack(x[e][j + 1] * up, x[e][j + 5] * up) : 0u;
   }
   const int src = 8 * R::head(tig);  // a lane whose column is the lane's head
-  qs[0] = __shfl_sync(0xffffffffu, sum[0] * up, src);
-  qs[1] = __shfl_sync(0xffffffffu, sum[1] * up, src);
-  return __uint_as_float((254u - __shfl_sync(0xffffffffu, f, src)) << 23);
+  qs[0] = __shfl_sync(0xffffffffu, sum[0] * up, src) * 0x1p-14f;
+  qs[1] = __shfl_sync(0xffffffffu, sum[1] * up, src) * 0x1p-14f;
+  return pow2(254 - (int)__shfl_sync(0xffffffffu, f, src));
 }
 
 // The pages of a warp's share. pos: first position + visible rows - 1 (a page's first position is a
@@ -217,8 +228,8 @@ struct Piece {
 };
 
 // One step over the two pages at `stage` (of a page with a negative entry no scale or minimum is used;
-// its codes are finite numbers whatever they are). kq undoes q's power of two and carries the softmax
-// scale in base 2; qs is sum q' of each group.
+// its codes are finite numbers whatever they are). kq undoes q's power of two and the codes' and carries the
+// softmax scale in base 2; qs is 2^-14 sum q' of each group.
 template <int G, bool kScores>
 __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry, const Piece& piece,
                                          const uint32_t (&qb)[8][2], float kq, const float (&qs)[2],
@@ -228,7 +239,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
   const int gid = lane >> 2, tig = lane & 3;
   const int myhead = R::head(tig), mypage = R::page(tig);
 
-  // ---- sums c[page] of c q': token gid groups 0, 1; token gid + 8 groups 0, 1 ----
+  // ---- sums c[page] of 2^-14 c q': token gid groups 0, 1; token gid + 8 groups 0, 1 ----
   float c[2][4];
   const unsigned char* kbase = stage + gid * kKv4RowBytes + 16 * tig;
 #pragma unroll
@@ -236,20 +247,20 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
     const uint4 wa = *reinterpret_cast<const uint4*>(kbase + n * kKv4PageBytes);
     const uint4 wb = *reinterpret_cast<const uint4*>(kbase + n * kKv4PageBytes + 8 * kKv4RowBytes);
     const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
-    // (the codes enter as c - 8; 8 sum q' brings that back, so c is sum c q')
+    // (the codes enter as 2^-14 (c - 8); 8 qs brings the 8 back, so c is 2^-14 sum c q')
     c[n][0] = c[n][2] = 8.f * qs[0];
     c[n][1] = c[n][3] = 8.f * qs[1];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t ca[4], cb[4];
-      codes_f16<8>(a[e], ca);
-      codes_f16<8>(b[e], cb);
+      codes_f16<8, true>(a[e], ca);
+      codes_f16<8, true>(b[e], cb);
       mma_16816_f16(c[n], ca[0], cb[0], ca[1], cb[1], qb[2 * e][0], qb[2 * e][1]);
       mma_16816_f16(c[n], ca[2], cb[2], ca[3], cb[3], qb[2 * e + 1][0], qb[2 * e + 1][1]);
     }
   }
 
-  // ---- this lane's scores x[page][token gid, gid + 8] (before kq) and the V meta of those tokens ----
+  // ---- this lane's scores x[page][token gid, gid + 8] and the V meta of those tokens ----
   const unsigned char* mbase = stage + mypage * kKv4PageBytes + kKv4MetaOff + gid * kKv4MetaBytes;
   float x[NM][2];
   uint32_t vm[NM][2][2];  // [page][token][group]
@@ -267,6 +278,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
         const uint32_t km = g ? m.y : m.x;
         x[n][i] = fmaf(kv4_scale(km), cc, g ? fmaf(kv4_min(km), qs[g], x[n][i]) : kv4_min(km) * qs[g]);
       }
+      x[n][i] *= kq;  // (rounded here once: what follows are differences of equal numbers)
     }
 
   const bool whole = (entry.x & entry.y & 15) == 15 && (entry.x | entry.y) >= 0;
@@ -290,7 +302,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
         float* dst = scores + (size_t)myhead * cap + (mine & ~15) + gid;
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // (what hides a row is looked up again: a score may be -inf)
-          if (whole || (mine >= 0 && row_visible(piece.plan, (mine & ~15) + gid + 8 * i))) dst[8 * i] = x[n][i] * kq;
+          if (whole || (mine >= 0 && row_visible(piece.plan, (mine & ~15) + gid + 8 * i))) dst[8 * i] = x[n][i];
       }
     }
   }
@@ -304,7 +316,6 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
   };
   float top = fmaxf(x[0][0], x[0][1]);
   if (NM == 2) top = fmaxf(top, fmaxf(x[NM - 1][0], x[NM - 1][1]));
-  top *= kq;
   if (__any_sync(0xffffffffu, top > st.m + kLazyMax)) {
     const float mx = over_head(top);
     const bool up = mx > st.m + kLazyMax;
@@ -333,7 +344,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
   for (int n = 0; n < NM; ++n)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float w = ex2_fast(fmaf(x[n][i], kq, -st.m));
+      const float w = ex2_fast(x[n][i] - st.m);
       st.l += w;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -626,7 +637,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
 
     uint32_t qb[8][2];
     float qs[2];
-    const float kq = prepare_q4<G>(qv, lane, qb, qs) * p.scale_log2;
+    const float kq = prepare_q4<G>(qv, lane, qb, qs) * 0x1p14f * p.scale_log2;
     float* scores = nullptr;
     if constexpr (kScores) scores = p.scores + ((size_t)b * p.hq + g * G) * p.cap;
 

@@ -1,5 +1,6 @@
 """Values at the ends of their ranges in decode over the 4-bit cache: a NaN that has to show however the
-history is shared out, V scales and scores that change along a warp's pages.
+history is shared out, V scales and scores that change along a warp's pages, scores and K
+of every magnitude.
 
 Tolerances are those of kv4_cases: a weight is off by a few ulp of its score, so where scores reach 8 times
 those of the other tests (128 in base 2) so does the bound, WIDE; outputs are measured against the range of
@@ -8,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv4_cases import MAX, SCALE, PagedCase, assert_lse_close, assert_out_close, full, gauss
+from kv4_cases import MAX, SCALE, PagedCase, assert_lse_close, assert_out_close, full, gauss, local
 from oracle import oda_oracle as O
 from sparse_kv_recall_b200 import build as B
 from sparse_kv_recall_b200 import oda
@@ -85,3 +86,51 @@ def test_v_rows_that_lost_their_weight_leave_the_others_exact(G, times, k):
     ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t))
     assert np.abs(out.double().cpu().numpy() - ref).max() <= MAX * WIDE
     assert np.abs(lse.double().cpu().numpy() - rlse).max() <= 1e-4 * WIDE
+
+
+@GROUPS
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("power", [10, 20, 52])
+def test_scores_of_every_magnitude(G, sign, power):
+    """K rows that are all alike: whatever the score (2^24 to 2^108 in base 2), every weight is 1 / n and the output
+    is the mean of V; the log-sum is the score to fp32's rounding. Lengths from one token up, hidden rows among
+    them; 29 pages in all, so that one CTA has them (between CTAs the weights go by fp32 log-sums, a unit of
+    which is more than 1 here)."""
+    lens = [1, 2, 17, 400]
+    v = gauss((sum(lens), 1, 128), 440)
+    k = torch.full((sum(lens), 1, 128), sign * 2.0 ** power, dtype=torch.bfloat16, device="cuda")
+    c = PagedCase(lens, G, 1, seed=441, rows=(k, v))
+    c.q.fill_(2.0 ** power)
+    for vis, pos in ((full(), lambda b, t: O.full_positions(t)), (local(3, 20), lambda b, t: O.local_positions(t, 3, 20))):
+        out, lse = _decode(c, vis)
+        ref, rlse, _ = c.oracle(pos)
+        assert_out_close(out, ref)
+        assert np.abs(lse.double().cpu().numpy() / rlse - 1).max() <= 2.0 ** -20
+
+
+@GROUPS
+@pytest.mark.parametrize("power", [-112, -40, 40, 110])
+def test_k_of_every_magnitude(G, power):
+    """q as far the other way: ordinary scores."""
+    lens = [5, 1500]
+    k = gauss((sum(lens), 2, 128), 442).float() * 2.0 ** power
+    c = PagedCase(lens, 2 * G, 2, seed=443, rows=(k.to(torch.bfloat16), gauss((sum(lens), 2, 128), 444)))
+    c.q.copy_((c.q.float() * 2.0 ** -power).to(torch.bfloat16))
+    out, lse = _decode(c)
+    ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t))
+    assert_out_close(out, ref)
+    assert_lse_close(lse.cpu().numpy(), rlse)
+
+
+@GROUPS
+@pytest.mark.parametrize("scale", [1e-8, 1e-30])
+def test_scores_that_vanish_hide_what_they_should(G, scale):
+    """q of zeros and a scale so small that its product with q's power of two is below fp32's range: every
+    visible weight is 1 / n, rows behind t and between sink and window stay hidden."""
+    lens = [1, 5, 17, 1000]
+    c = PagedCase(lens, 2 * G, 2, seed=445)
+    c.q.zero_()
+    ref, rlse, _ = c.oracle(lambda b, t: O.local_positions(t, 3, 20))
+    out, lse = _decode(c, local(3, 20), scale)
+    assert_out_close(out, ref)
+    assert_lse_close(lse.cpu().numpy(), rlse)
