@@ -46,6 +46,7 @@ constexpr int kStageBytes4 = kPages4 * kKv4PageBytes;
 constexpr int kRefs4 = 64;           // page references a warp holds (two halves, refilled in turn)
 constexpr int kCtasPerSm4 = 2;
 constexpr int kMinShare4 = 32;       // pages per CTA at least (two steps a warp)
+constexpr float kMergeRoom = 10.f;   // partials are weighed by 2^-10 and less: there are fewer than 2^10
 constexpr int kPStride = 48;         // words per (page, head) of the weight exchange
 constexpr int kPWords = 2 * 4 * kPStride;
 
@@ -140,7 +141,7 @@ struct Roles {
 };
 
 struct Kv4State {
-  float m, l;          // running maximum (base 2) and this lane's part of the softmax sum
+  float m, l;          // base-2 reference of the weights and this lane's part of the softmax sum
   float corr[2];       // this lane's part of sum w (M_g + z S_g)
   float r[2];          // w S_g enters the tensor cores times this power of two
   float acc[8][4];     // tile 4 g + j: dims 64 g + 8 gid + j (0, 1) and + j + 4 (2, 3); columns
@@ -151,7 +152,9 @@ constexpr int kRTop = 253;             // exponent field of r at its largest, 2^
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)e << 23); }
 __device__ __forceinline__ int pow2_exp(float x) { return (int)(__float_as_uint(x) >> 23); }
 
-constexpr float kNoMax = -3.4028234e38f;  // running maximum before any visible score: below every other
+constexpr float kNoMax = -3.4028234e38f;  // m before any visible score: below every other
+constexpr float kRoom = 7.f;  // scores stay this far below m: a weight times a scale or a value, and the sum of some
+                              // hundred of them, is inside fp32 for the largest bf16 values too
 
 // The group's q as B fragments (scaled to q') and, for the lane's own head, 2^-14 sum q' of each group and the
 // factor that undoes q's power of two and the codes' 2^-14. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
@@ -307,7 +310,7 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
     }
   }
 
-  // ---- online softmax; the maximum is raised only when a score passes it by 2^kLazyMax ----
+  // ---- online softmax; m is raised only when a score comes within kRoom of it, to kRoom + kLazyMax above ----
   auto over_head = [&](float v) {  // maximum over the lanes that hold the head
     if (NM == 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
@@ -316,11 +319,11 @@ __device__ __forceinline__ void kv4_step(const unsigned char* stage, int2 entry,
   };
   float top = fmaxf(x[0][0], x[0][1]);
   if (NM == 2) top = fmaxf(top, fmaxf(x[NM - 1][0], x[NM - 1][1]));
-  if (__any_sync(0xffffffffu, top > st.m + kLazyMax)) {
+  if (__any_sync(0xffffffffu, top > st.m - kRoom)) {
     const float mx = over_head(top);
-    const bool up = mx > st.m + kLazyMax;
-    const float d = up ? mx - st.m : 0.f, al = ex2_fast(-d);
-    if (up) st.m = mx;
+    const float m = mx > st.m - kRoom ? mx + (kRoom + kLazyMax) : st.m;
+    const float d = m - st.m, al = ex2_fast(-d);
+    st.m = m;
     st.l *= al;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
@@ -787,6 +790,7 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
           if (__any_sync(0xffffffffu, any) && m == -INFINITY) m = 0.f;  // (NaNs alone: the weights are NaN)
+          m += kMergeRoom;  // (the sum over the partials stays below the largest of them)
 #pragma unroll 1
           for (int s = lane; s < n_contrib; s += 32) {
             const float ls = sw[s * G + warp];

@@ -1,5 +1,5 @@
 """Values at the ends of their ranges in decode over the 4-bit cache: a NaN that has to show however the
-history is shared out, V scales and scores that change along a warp's pages, scores and K
+history is shared out, V scales and scores that change along a warp's pages, scores, K and V
 of every magnitude.
 
 Tolerances are those of kv4_cases: a weight is off by a few ulp of its score, so where scores reach 8 times
@@ -86,6 +86,38 @@ def test_v_rows_that_lost_their_weight_leave_the_others_exact(G, times, k):
     ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t))
     assert np.abs(out.double().cpu().numpy() - ref).max() <= MAX * WIDE
     assert np.abs(lse.double().cpu().numpy() - rlse).max() <= 1e-4 * WIDE
+
+
+@GROUPS
+@pytest.mark.parametrize("power", [-105, 123])
+def test_v_of_every_magnitude(G, power):
+    """The largest rows reach 2^125.5, the span of a group 2^126.5. Scores are 7.1 in base 2 higher in every
+    other run of 256 positions: just not enough for the softmax to take a new maximum."""
+    n, hkv = 1500, 2
+    k, v = gauss((n, hkv, 128), 432).float(), gauss((n, hkv, 128), 430).float() * 2.0 ** power
+    k[..., 0] = torch.where(torch.arange(n, device="cuda") // 256 % 2 == 0, 0.0, 3.5).view(-1, 1)
+    c = PagedCase([n], G * hkv, hkv, seed=431, rows=(k.to(torch.bfloat16), v.to(torch.bfloat16)))
+    c.q[..., 0] = 16.0
+    out, lse = _decode(c)
+    ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t))
+    assert np.abs(out.double().cpu().numpy() - ref).max() <= MAX * 2.0 ** power
+    assert_lse_close(lse.cpu().numpy(), rlse)
+
+
+@GROUPS
+@pytest.mark.parametrize("n", [1, 40, 3000, 40000])
+def test_v_rows_of_the_largest_value(G, n):
+    """Every weight alike, every value the largest bf16 (0.4 % below the largest fp32): the mean is that value, to
+    the rounding of the sums (n 2^-24 at the very most, in fact a few ulp: 1e-5)."""
+    big = float(torch.finfo(torch.bfloat16).max)
+    v = torch.full((n, 1, 128), big, dtype=torch.bfloat16, device="cuda")
+    v[..., 64:] = -big
+    c = PagedCase([n], G, 1, seed=433, rows=(gauss((n, 1, 128), 434), v))
+    c.q.zero_()
+    out, lse = _decode(c)
+    assert (out[..., :64].double() / big - 1).abs().max() <= 1e-5
+    assert (out[..., 64:].double() / -big - 1).abs().max() <= 1e-5
+    assert (lse.double() - np.log(n)).abs().max() <= 1e-5
 
 
 @GROUPS
