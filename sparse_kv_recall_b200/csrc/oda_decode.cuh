@@ -677,6 +677,9 @@ __device__ __forceinline__ void decode_pass(const DecodeParams& p, const SplitSm
         v += __shfl_xor_sync(0xffffffffu, v, 2);
       }
       lsum[u] = v;
+      // (scores that are NaN alone raise no maximum; -inf would make them an empty set at the merges)
+      if constexpr (kScores)
+        if (m_run[u] == -INFINITY && isnan(v)) m_run[u] = 0.f;
     }
     if (p.stats != nullptr && lane == 0 && (rows_vis | pages_read)) {
       atomicAdd(sm.s_rows, (unsigned long long)rows_vis);
@@ -791,6 +794,11 @@ __device__ __forceinline__ void decode_pass(const DecodeParams& p, const SplitSm
           for (int s = lane; s < n_contrib; s += 32) m = fmaxf(m, sw[s * G + warp]);
 #pragma unroll
           for (int o2 = 16; o2 >= 1; o2 >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o2));
+          if constexpr (kScores) {
+            bool any = false;  // a maximum passes over a NaN; NaNs alone are no empty set
+            for (int s = lane; s < n_contrib; s += 32) any |= sw[s * G + warp] != -INFINITY;
+            if (__any_sync(0xffffffffu, any) && m == -INFINITY) m = 0.f;
+          }
           float sum = 0.f;
           for (int s = lane; s < n_contrib; s += 32) {
             const float ls = sw[s * G + warp];

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv4_cases import MAX, SCALE, PagedCase, assert_lse_close, assert_out_close, full, gauss, local
+from kv4_cases import MASS, MAX, SCALE, PagedCase, assert_lse_close, assert_out_close, full, gauss, local
 from oracle import oda_oracle as O
 from sparse_kv_recall_b200 import build as B
 from sparse_kv_recall_b200 import oda
@@ -166,3 +166,25 @@ def test_scores_that_vanish_hide_what_they_should(G, scale):
     out, lse = _decode(c, local(3, 20), scale)
     assert_out_close(out, ref)
     assert_lse_close(lse.cpu().numpy(), rlse)
+
+
+@GROUPS
+@pytest.mark.parametrize("kv4", [False, True])
+def test_a_nan_in_q_shows_in_the_weights(kv4, G):
+    """In the output, log-sum and weights of its own head and KV head alone, from one CTA to many."""
+    lens = [1, 50, 3000]
+    c = PagedCase(lens, 2 * G, 2, seed=450, kv4=kv4)
+    ref, rlse, want = c.oracle(lambda b, t: O.full_positions(t))
+    last = 2 * G - 1
+    c.q[:, last, 77] = float("nan")
+    out, lse = c.out(fill=3.0)
+    mass = torch.full((3, 2, c.maxb * 16), 2.0, device="cuda")
+    call = oda.oda_kv4_decode_mass if kv4 else oda.oda_decode_mass
+    call(c.kv, full(), c.q, SCALE, out, c.ws, mass, mass_in=mass, lse=lse)
+    c.ok()
+    assert torch.isnan(out[:, last]).all() and torch.isnan(lse[:, last]).all()
+    assert_out_close(out[:, :last], ref[:, :last])
+    assert_lse_close(lse[:, :last].cpu().numpy(), rlse[:, :last])
+    for b, n in enumerate(lens):
+        assert torch.isnan(mass[b, 1, :n]).all() and (mass[b, :, n:] == 2.0).all()
+        assert np.abs(mass[b, 0, :n].double().cpu().numpy() - 2.0 - want[b][1][0]).max() <= MASS + 2.0 ** -22
