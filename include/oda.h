@@ -345,9 +345,10 @@ int oda_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q, 
  * keep their contents. mass_in, mass_out: fp32 [batch][num_kv_heads][mass_tokens], 16-byte aligned,
  * mass_tokens a multiple of 4 and at least 16 * max_blocks_per_seq. mass_in may be mass_out (only
  * visible positions are then touched) or NULL (zero); it may not overlap it otherwise. ws: at least the
- * matching workspace size (it holds a score per query head and position), zeroed once; that of
- * oda_decode_mass is for one batch, head count and max_blocks_per_seq (its tickets lie where another's
- * scores may: zero it again for others), that of oda_kv4_decode_mass for any. With a keep list
+ * matching workspace size (it holds a score per query head and position: 4 * batch * num_q_heads * 16 *
+ * max_blocks_per_seq bytes and little else), zeroed once; it serves calls of any batch, head counts and
+ * max_blocks_per_seq it is large enough for, one behind the other. A call of the other cache kind needs a
+ * workspace of its own or one zeroed again. With a keep list
  * that is not strictly ascending the sequence's mass is unspecified. Calls that may overlap on the GPU need
  * a workspace each. Two kernel launches. */
 int oda_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,

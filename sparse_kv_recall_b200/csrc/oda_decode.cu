@@ -572,12 +572,14 @@ static int launch_scores_kernel(const DecodeParams& p, const DeviceInfo& di, cud
 
 int launch_decode_scores(const oda_kv* kv, const oda_visibility& vis, const void* q, int hq,
                          float scale, const void* k_new, const void* v_new, void* out, int out_dtype,
-                         float* lse, float* scores, int cap, void* ws, size_t ws_bytes, void* stream) {
+                         float* lse, float* scores, int cap, unsigned* tickets, void* ws, size_t ws_bytes,
+                         void* stream) {
   DecodeParams p;
   int rc = decode_params(kv, vis, q, hq, scale, k_new, v_new, out, out_dtype, lse, ws, ws_bytes, &p);
   if (rc != ODA_OK || kv->batch == 0) return rc;
   p.scores = scores;
   p.score_cap = cap;
+  p.ws_ticket = tickets;
   DeviceInfo di;
   if ((rc = current_device_info(&di)) != ODA_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -602,6 +604,14 @@ int decode_ws_layout(int batch, int hkv, int hq, size_t* total, size_t* ticket_o
   const WsLayout wl = ws_layout(batch, hkv, hq / hkv, grid_size(di));
   *total = wl.total;
   *ticket_off = wl.ticket_off;
+  return ODA_OK;
+}
+
+int decode_scores_tickets_bytes(size_t* bytes) {
+  DeviceInfo di;
+  const int rc = current_device_info(&di);
+  if (rc != ODA_OK) return rc;
+  *bytes = align_up(grid_size(di) * sizeof(unsigned), 256);
   return ODA_OK;
 }
 

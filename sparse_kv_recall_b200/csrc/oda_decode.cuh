@@ -762,7 +762,9 @@ __device__ __forceinline__ void decode_pass(const DecodeParams& p, const SplitSm
         if (tid == 0) p.ws_lse[slot * G + gg] = l2[gg];
       }
       __syncthreads();  // the CTA's partial is written; thread 0 publishes it (release)
-      if (tid == 0) *sm.s_last = ticket_arrive(&p.ws_ticket[bg]) == (unsigned)(n_contrib - 1);
+      // (with scores, the ticket of the CTA the (b, g) begins in: only the last that begins there is shared)
+      unsigned int* const ticket = &p.ws_ticket[kScores ? c_first : bg];
+      if (tid == 0) *sm.s_last = ticket_arrive(ticket) == (unsigned)(n_contrib - 1);
       __syncthreads();  // ... and the last CTA's thread 0 acquired everyone's partials
       if (*sm.s_last) {
         // Merge the n_contrib partials in fixed order: log-sums into shared memory (stage
@@ -842,7 +844,7 @@ __device__ __forceinline__ void decode_pass(const DecodeParams& p, const SplitSm
           }
         }
         write_final<G>(p, b, g, o, l2);
-        if (tid == 0) p.ws_ticket[bg] = 0u;  // leave the workspace zeroed
+        if (tid == 0) *ticket = 0u;  // leave the workspace zeroed
       }
     }
     fence_proxy_async_smem();  // merge scratch is the next piece's stage memory

@@ -50,10 +50,13 @@ int check_decode_args(const oda_kv* kv, const oda_visibility& vis, const void* q
                       const float* lse, const void* ws);
 
 // Decode launch that also stores the base-2 score of every visible position: scores fp32
-// [batch][hq][cap], the rest unwritten. Lets a dependent launch start early.
+// [batch][hq][cap], the rest unwritten. Lets a dependent launch start early. Its merge tickets, one per CTA and
+// zeroed once, are apart from the decode workspace: how many there are depends on the device alone.
+int decode_scores_tickets_bytes(size_t* bytes);
 int launch_decode_scores(const oda_kv* kv, const oda_visibility& vis, const void* q, int hq,
                          float scale, const void* k_new, const void* v_new, void* out, int out_dtype,
-                         float* lse, float* scores, int cap, void* ws, size_t ws_bytes, void* stream);
+                         float* lse, float* scores, int cap, unsigned* tickets, void* ws, size_t ws_bytes,
+                         void* stream);
 
 // 4-bit caches: the same page table and lengths as an oda_kv (its caches both point at the
 // codes), checks, workspace and launch of the decode kernel (scores nullable, as above).

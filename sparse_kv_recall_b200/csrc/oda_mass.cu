@@ -124,23 +124,29 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassParams p) 
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Workspace: the decode call's, a log-sum per query head, the scores.
-static int mass_ws(int batch, int hkv, int hq, int max_blocks, bool kv4, size_t* decode, size_t* lse_off,
-                   size_t* scores_off, size_t* total) {
+// Workspace: merge tickets (the 4-bit decode's lie in front of its own workspace), the decode call's, a log-sum per
+// query head, the scores. The tickets are in the same place for every shape and nothing else has to be
+// zero, so one workspace serves calls of any.
+struct MassWs {
+  size_t decode_off, decode, lse_off, scores_off, total;
+};
+static int mass_ws(int batch, int hkv, int hq, int max_blocks, bool kv4, MassWs* w) {
   if (batch < 0 || hkv < 1 || hq < 1 || max_blocks < 1) return ODA_ERR_INVALID_ARG;
   int rc;
+  w->decode_off = 0;
   if (kv4) {
-    rc = kv4_decode_ws_bytes(batch, hkv, hq, decode);
+    rc = kv4_decode_ws_bytes(batch, hkv, hq, &w->decode);
   } else {
     size_t ticket = 0;
     rc = hq % hkv != 0 || (hq / hkv != 1 && hq / hkv != 2 && hq / hkv != 4)
              ? ODA_ERR_UNSUPPORTED_SHAPE
-             : decode_ws_layout(batch, hkv, hq, decode, &ticket);
+             : decode_ws_layout(batch, hkv, hq, &w->decode, &ticket);
+    if (rc == ODA_OK) rc = decode_scores_tickets_bytes(&w->decode_off);
   }
   if (rc != ODA_OK) return rc;
-  *lse_off = up256(*decode);
-  *scores_off = *lse_off + up256((size_t)batch * hq * sizeof(float));
-  *total = *scores_off + (size_t)batch * hq * max_blocks * kPage * sizeof(float);
+  w->lse_off = w->decode_off + up256(w->decode);
+  w->scores_off = w->lse_off + up256((size_t)batch * hq * sizeof(float));
+  w->total = w->scores_off + (size_t)batch * hq * max_blocks * kPage * sizeof(float);
   return ODA_OK;
 }
 
@@ -160,20 +166,20 @@ static int decode_mass(const oda_kv* kv, const oda_kv4* kv4, const oda_visibilit
   if (kv->batch == 0) return ODA_OK;
   if (mass_out == nullptr || !aligned_or_null(mass_out, 16) || !aligned_or_null(mass_in, 16))
     return ODA_ERR_INVALID_ARG;
-  size_t decode = 0, lse_off = 0, scores_off = 0, total = 0;
-  rc = mass_ws(kv->batch, kv->num_kv_heads, hq, kv->max_blocks_per_seq, kv4 != nullptr, &decode, &lse_off,
-               &scores_off, &total);
+  MassWs wl;
+  rc = mass_ws(kv->batch, kv->num_kv_heads, hq, kv->max_blocks_per_seq, kv4 != nullptr, &wl);
   if (rc != ODA_OK) return rc;
-  if (ws_bytes < total) return ODA_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < wl.total) return ODA_ERR_WORKSPACE_TOO_SMALL;
   const long long blocks_per_row = (cap + 4 * kMassThreads - 1) / (4 * kMassThreads);
   if (blocks_per_row * kv->batch * kv->num_kv_heads >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
   unsigned char* w = static_cast<unsigned char*>(ws);
-  float* l = lse != nullptr ? lse : reinterpret_cast<float*>(w + lse_off);
-  float* scores = reinterpret_cast<float*>(w + scores_off);
+  float* l = lse != nullptr ? lse : reinterpret_cast<float*>(w + wl.lse_off);
+  float* scores = reinterpret_cast<float*>(w + wl.scores_off);
   rc = kv4 != nullptr ? launch_kv4_decode(kv4, vis, q, hq, scale, k_new, v_new, out, out_dtype, l, scores,
-                                          (int)cap, ws, decode, stream)
+                                          (int)cap, w + wl.decode_off, wl.decode, stream)
                       : launch_decode_scores(kv, *vis, q, hq, scale, k_new, v_new, out, out_dtype, l,
-                                             scores, (int)cap, ws, decode, stream);
+                                             scores, (int)cap, reinterpret_cast<unsigned*>(w),
+                                             w + wl.decode_off, wl.decode, stream);
   if (rc != ODA_OK) return rc;
 
   MassParams p;
@@ -197,21 +203,23 @@ static int decode_mass(const oda_kv* kv, const oda_kv4* kv4, const oda_visibilit
 
 using namespace oda;
 
+static int mass_ws_size(int batch, int hkv, int hq, int max_blocks, bool kv4, size_t* bytes) {
+  if (bytes == nullptr) return ODA_ERR_INVALID_ARG;
+  MassWs w;
+  const int rc = mass_ws(batch, hkv, hq, max_blocks, kv4, &w);
+  if (rc == ODA_OK) *bytes = w.total;
+  return rc;
+}
+
 extern "C" int oda_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
                                               int32_t max_blocks_per_seq, size_t* bytes) {
-  size_t d, l, s;
-  return bytes == nullptr ? ODA_ERR_INVALID_ARG
-                          : mass_ws(batch, num_kv_heads, num_q_heads, max_blocks_per_seq, false, &d, &l, &s,
-                                    bytes);
+  return mass_ws_size(batch, num_kv_heads, num_q_heads, max_blocks_per_seq, false, bytes);
 }
 
 extern "C" int oda_kv4_decode_mass_workspace_size(int32_t batch, int32_t num_kv_heads,
                                                   int32_t num_q_heads, int32_t max_blocks_per_seq,
                                                   size_t* bytes) {
-  size_t d, l, s;
-  return bytes == nullptr ? ODA_ERR_INVALID_ARG
-                          : mass_ws(batch, num_kv_heads, num_q_heads, max_blocks_per_seq, true, &d, &l, &s,
-                                    bytes);
+  return mass_ws_size(batch, num_kv_heads, num_q_heads, max_blocks_per_seq, true, bytes);
 }
 
 extern "C" int oda_decode_mass(const oda_kv* kv, const oda_visibility* vis, const void* q,

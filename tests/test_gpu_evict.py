@@ -470,3 +470,27 @@ def test_sequences_that_share_a_prefix_are_cut_apart(kv4):
     _assert_evicted(c, lens, dst, old, old_mass, kept, mass_out, new_lens, 4, 16, budget)
     src = torch.unique(c.bt[c.bt >= 0]).long()
     assert torch.equal(c.raw()[src], raw[src]) if kv4 else torch.equal(c.raw()[:, src], raw[:, src])
+
+
+@BOTH
+def test_one_workspace_for_weights_of_every_shape(kv4):
+    """Batches, head counts and table widths in turn over one workspace, with (sequence, KV head)s that begin and end
+    inside a CTA's share; each call as with a workspace of its own."""
+    cases = [PagedCase([9000], 4, 1, seed=160, kv4=kv4), PagedCase([700, 3, 2100, 44], 16, 4, seed=161, kv4=kv4),
+             PagedCase([2000 + 17 * i for i in range(24)], 8, 8, seed=162, kv4=kv4),
+             PagedCase([6000, 12000], 6, 3, seed=163, kv4=kv4)]
+    refs = []
+    for c in cases:
+        (out, lse), mass = c.out(), torch.zeros((c.B, c.hkv, c.maxb * 16), device="cuda")
+        _mass_call(c)(c.kv, full(), c.q, SCALE, out, c.ws, mass, lse=lse)
+        c.ok()
+        refs.append((out, lse, mass))
+    ref, rlse, _ = cases[2].oracle(lambda b, t: O.full_positions(t))
+    assert_out_close(refs[2][0], ref)
+    ws = torch.zeros(max(c.ws.numel() for c in cases), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 3, 2, 0, 3, 1, 1, 2, 0):
+        c = cases[i]
+        (out, lse), mass = c.out(), torch.zeros_like(refs[i][2])
+        _mass_call(c)(c.kv, full(), c.q, SCALE, out, ws, mass, lse=lse)
+        c.ok()
+        assert all(torch.equal(a, b) for a, b in zip((out, lse, mass), refs[i])), i
