@@ -16,7 +16,7 @@ namespace oda {
 
 constexpr int kRowWarps = 4;                       // (101,488 units appended: 17.6 us with 4, 18.2 with 8, 19.8 with 16)
 constexpr int kMany = 8;                           // units a warp takes where there are many:
-constexpr int kManyUnits = kMany * 8 * 148;        // enough for eight such warps per SM
+constexpr int kManyWarps = 8;                      // ... to give every SM this many such warps
 
 struct RowsParams {
   unsigned char* cache;
@@ -267,21 +267,16 @@ int check_kv4(const oda_kv4* kv) {
   return kv->max_blocks_per_seq >= (1 << 27) ? ODA_ERR_UNSUPPORTED_SHAPE : ODA_OK;  // 32-bit positions
 }
 
-// Host checks shared by append and read; *grid is 0 when there is nothing to do.
+// Host checks shared by append and read; *work is false when there is nothing to do.
 static int rows_params(const oda_kv4* kv, int32_t num_rows, const int32_t* cu_rows,
-                       const int32_t* gate, RowsParams* p, unsigned* grid, bool* many) {
-  *grid = 0;
+                       const int32_t* gate, RowsParams* p, bool* work) {
+  *work = false;
   const int rc = check_kv4(kv);
   if (rc != ODA_OK) return rc;
   if (num_rows < 0 || (cu_rows == nullptr && num_rows != kv->batch)) return ODA_ERR_INVALID_ARG;
   if (!aligned_or_null(cu_rows, 4) || !aligned_or_null(gate, 4)) return ODA_ERR_INVALID_ARG;
   if (kv->batch == 0 || num_rows == 0) return ODA_OK;
   if (num_rows > 0x7fff0000) return ODA_ERR_UNSUPPORTED_SHAPE;  // (the last warps' rows pass num_rows)
-  const long long units = (long long)num_rows * kv->num_kv_heads;
-  *many = units >= kManyUnits;
-  const long long per_cta = kRowWarps * (*many ? kMany : 1);
-  const long long blocks = (units + per_cta - 1) / per_cta;
-  if (blocks >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
   p->cache = static_cast<unsigned char*>(kv->cache);
   p->block_table = kv->block_table;
   p->seq_lens = kv->seq_lens;
@@ -293,6 +288,20 @@ static int rows_params(const oda_kv4* kv, int32_t num_rows, const int32_t* cu_ro
   p->num_rows = num_rows;
   p->gate = gate;
   p->status = kv->dev_status;
+  *work = true;
+  return ODA_OK;
+}
+
+// CTAs, and whether a warp takes kMany units.
+static int rows_grid(const RowsParams& p, unsigned* grid, bool* many) {
+  DeviceInfo di;
+  const int rc = current_device_info(&di);
+  if (rc != ODA_OK) return rc;
+  const long long units = (long long)p.num_rows * p.hkv;
+  *many = units >= (long long)kMany * kManyWarps * di.sms;
+  const long long per_cta = kRowWarps * (*many ? kMany : 1);
+  const long long blocks = (units + per_cta - 1) / per_cta;
+  if (blocks >= (1ll << 31)) return ODA_ERR_UNSUPPORTED_SHAPE;
   *grid = (unsigned)blocks;
   return ODA_OK;
 }
@@ -305,17 +314,19 @@ extern "C" int oda_kv4_append(const oda_kv4* kv, const void* k_new, const void* 
                               int64_t k_stride, int64_t v_stride, int32_t num_rows,
                               const int32_t* cu_rows, const int32_t* gate, void* stream) {
   RowsParams p;
-  unsigned grid;
-  bool many = false;
-  const int rc = rows_params(kv, num_rows, cu_rows, gate, &p, &grid, &many);
+  bool work;
+  int rc = rows_params(kv, num_rows, cu_rows, gate, &p, &work);
   if (rc != ODA_OK) return rc;
   const int64_t row = (int64_t)kv->num_kv_heads * kHeadDim;
   if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
     return ODA_ERR_INVALID_ARG;  // rows are read 16 bytes at a time
-  if (grid == 0) return ODA_OK;
+  if (!work) return ODA_OK;
   if (k_new == nullptr || v_new == nullptr || !aligned_or_null(k_new, 16) ||
       !aligned_or_null(v_new, 16))
     return ODA_ERR_INVALID_ARG;
+  unsigned grid;
+  bool many;
+  if ((rc = rows_grid(p, &grid, &many)) != ODA_OK) return rc;
   return cuda_status(launch_dependent(
       many ? kv4_append_many_kernel<kMany> : kv4_append_kernel, grid, kRowWarps * 32, 0,
       static_cast<cudaStream_t>(stream), p, static_cast<const __nv_bfloat16*>(k_new),
@@ -325,15 +336,17 @@ extern "C" int oda_kv4_append(const oda_kv4* kv, const void* k_new, const void* 
 extern "C" int oda_kv4_read(const oda_kv4* kv, void* k_out, void* v_out, int32_t out_dtype,
                             int32_t num_rows, const int32_t* cu_rows, void* stream) {
   RowsParams p;
-  unsigned grid;
-  bool many = false;
-  const int rc = rows_params(kv, num_rows, cu_rows, nullptr, &p, &grid, &many);
+  bool work;
+  int rc = rows_params(kv, num_rows, cu_rows, nullptr, &p, &work);
   if (rc != ODA_OK) return rc;
   if (out_dtype != ODA_F32 && out_dtype != ODA_BF16) return ODA_ERR_INVALID_ARG;
-  if (grid == 0) return ODA_OK;
+  if (!work) return ODA_OK;
   if (k_out == nullptr || v_out == nullptr || !aligned_or_null(k_out, 16) ||
       !aligned_or_null(v_out, 16))
     return ODA_ERR_INVALID_ARG;
+  unsigned grid;
+  bool many;
+  if ((rc = rows_grid(p, &grid, &many)) != ODA_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const auto kernel = out_dtype == ODA_BF16
                           ? (many ? kv4_read_many_kernel<kMany, true> : kv4_read_kernel<true>)
