@@ -404,6 +404,17 @@ def make_kv4(cache, block_table, seq_lens, dev_status=None, stats=None) -> oda_k
     nb, hkv, nbytes = cache.shape
     if nbytes != ODA_KV4_PAGE_BYTES:
         raise ValueError("cache pages must be %d bytes, got %d" % (ODA_KV4_PAGE_BYTES, nbytes))
+    # (the kernels read and write these by the cache's batch and on its device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape (batch, blocks), got %s" % (tuple(block_table.shape),))
+    _shape(seq_lens, (block_table.shape[0],), "seq_lens")
+    for t, least, name in ((dev_status, 1, "dev_status"), (stats, ODA_STATS_LEN, "stats")):
+        if t is not None and t.numel() < least:
+            raise ValueError("%s must have %d elements, got %d" % (name, least, t.numel()))
+    for t, name in ((block_table, "block_table"), (seq_lens, "seq_lens"), (dev_status, "dev_status"),
+                    (stats, "stats")):
+        if t is not None and t.device != cache.device:
+            raise ValueError("%s must be on the cache's device %s, got %s" % (name, cache.device, t.device))
     kv = oda_kv4(
         cache=_ptr(cache, torch.uint8, "cache"),
         block_table=_ptr(block_table, torch.int32, "block_table"),

@@ -141,3 +141,22 @@ def test_wrappers_refuse_host_tensors_and_wrong_shapes():
                           torch.zeros(2, 2, 64), torch.zeros(2), torch.zeros(8))
     with pytest.raises(ValueError, match="2304"):
         oda.make_kv4(torch.zeros(2, 2, 2048, dtype=torch.uint8), torch.zeros(2, 2), torch.zeros(2))
+
+
+def test_make_kv4_refuses_tables_that_do_not_fit():
+    """Lengths, status and counters are read and written by the batch, on the cache's device."""
+    cache, table, lens = (torch.zeros(2, 2, 2304, dtype=torch.uint8), torch.zeros(3, 4, dtype=torch.int32),
+                          torch.zeros(3, dtype=torch.int32))
+    for bad in (lens[:2], lens.view(3, 1), torch.zeros((), dtype=torch.int32)):
+        with pytest.raises(ValueError, match="seq_lens"):
+            oda.make_kv4(cache, table, bad)
+    with pytest.raises(ValueError, match="block_table"):
+        oda.make_kv4(cache, table[0], lens)
+    with pytest.raises(ValueError, match="dev_status"):
+        oda.make_kv4(cache, table, lens, dev_status=torch.zeros(0, dtype=torch.int32))
+    with pytest.raises(ValueError, match="stats"):
+        oda.make_kv4(cache, table, lens, stats=torch.zeros(1, dtype=torch.int64))
+    with pytest.raises(ValueError, match="device"):
+        oda.make_kv4(cache, table, lens.to("meta"))
+    with pytest.raises(ValueError, match="CUDA"):
+        oda.make_kv4(cache, table, lens)
