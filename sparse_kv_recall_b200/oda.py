@@ -499,7 +499,7 @@ def _row_stride(t, hkv: int, dev: int, name) -> int:
     s, h, d = t.stride()
     if d != 1 or (hkv > 1 and h != 128):
         raise ValueError("%s: heads and dims must be dense" % name)
-    return s if n > 1 else max(s, hkv * 128)
+    return s if n > 1 else hkv * 128  # (of one row, whatever its tensor's stride says)
 
 
 def _cu_rows(kv, cu_rows, num_rows, dev):

@@ -521,3 +521,16 @@ def test_one_workspace_for_calls_of_every_shape():
         c.ok()
         assert torch.equal(out, o) and torch.equal(lse, l), i
         assert torch.equal(out2, o) and torch.equal(lse2, l) and torch.equal(got, m), i
+
+
+def test_append_of_one_row_takes_any_row_stride():
+    """A single row's stride says nothing: one that is no multiple of 8 elements is no reason to refuse it."""
+    c = PagedCase([20], 8, 4, seed=95)
+    k, v = (gauss((4 * 128,), 96 + i).as_strided((1, 4, 128), (4 * 128 + 4, 128, 1)) for i in range(2))
+    assert k.stride(0) % 8 != 0
+    oda.oda_kv4_append(c.kv, k, v)
+    back = [torch.empty(1, 4, 128, device="cuda") for _ in range(2)]
+    oda.oda_kv4_read(c.kv, *back)
+    c.ok()
+    for got, want in zip(back, (k, v)):
+        assert np.array_equal(got.cpu().numpy(), K.round_trip(want.double().cpu().numpy()).astype(np.float32))
