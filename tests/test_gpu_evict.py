@@ -494,3 +494,42 @@ def test_one_workspace_for_weights_of_every_shape(kv4):
         _mass_call(c)(c.kv, full(), c.q, SCALE, out, ws, mass, lse=lse)
         c.ok()
         assert all(torch.equal(a, b) for a, b in zip((out, lse, mass), refs[i])), i
+
+
+@BOTH
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("budget", [700, 9000])
+def test_evict_more_slots_than_a_cta_holds_keys_of(kv4, ties, in_place, budget):
+    """One CTA a (sequence, KV head), 160 of them: of 8193 and 20,011 slots the keys do not fit in shared memory and the
+    kept list goes through its output."""
+    lens = [8193, 20011, 8192] + [30 + i for i in range(17)]
+    need = [-(-min(n, budget) // 16) for n in lens]
+    c = PagedCase(lens, 8, 8, seed=170, kv4=kv4, spare=0 if in_place else sum(need))
+    mass = _random_mass(c, 171, ties)
+    if ties:                                       # and many that were never attended
+        mass[:, :, 100:15000:3] = 0.0
+    old, old_mass = (c.k.copy(), c.v.copy()), mass.clone()
+    dst = None
+    if not in_place:                               # entries behind what is kept are not looked at
+        dst = torch.full((len(lens), -(-budget // 16)), -1, dtype=torch.int32, device="cuda")
+        for row, own in zip(dst, c.spare.split(need)):
+            row[:len(own)] = own
+    kept, mass_out, new_lens = _evict(c, mass, 4, 300, budget, dst)
+    c.ok()
+    _assert_evicted(c, lens, c.bt if in_place else dst, old, old_mass, kept, mass_out, new_lens, 4, 300, budget)
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_more_slots_than_a_cluster_holds_keys_of(ties, in_place):
+    """16 CTAs of 8192 keys hold 131,072: of one sequence of 140,003 slots every pass reads the weights again."""
+    n, budget = 140003, 50000
+    pages = -(-budget // 16)
+    c = PagedCase([n], 1, 1, seed=172, spare=0 if in_place else pages)
+    mass = _random_mass(c, 173, ties)
+    old, old_mass = (c.k.copy(), c.v.copy()), mass.clone()
+    dst = None if in_place else c.spare.view(1, pages).contiguous()
+    kept, mass_out, new_lens = _evict(c, mass, 4, 2000, budget, dst)
+    c.ok()
+    _assert_evicted(c, [n], c.bt if in_place else dst, old, old_mass, kept, mass_out, new_lens, 4, 2000, budget)
