@@ -341,9 +341,10 @@ int oda_kv4_decode(const oda_kv4* kv, const oda_visibility* vis, const void* q, 
  * oda_decode / oda_kv4_decode, and
  *   mass_out[b][g][p] = mass_in[b][g][p] + sum over the query heads of KV head g of the softmax weight of
  *                       position p (0 where p is not visible)
- * for 0 <= p < seq_lens[b]. Rows that are not visible may hold anything, NaN included, as in oda_kv4_decode
- * (oda_decode itself weighs a hidden V row of a page it reads by zero: it has to be finite). Other positions, and the rows of a sequence that is gated off or in error,
- * keep their contents. mass_in, mass_out: fp32 [batch][num_kv_heads][mass_tokens], 16-byte aligned,
+ * for 0 <= p < seq_lens[b]; other positions, and the rows of a sequence that is gated off or in error,
+ * keep their contents. Rows that are not visible may hold anything, NaN included, as in oda_kv4_decode
+ * (oda_decode itself weighs a hidden V row of a page it reads by zero: it has to be finite). mass_in,
+ * mass_out: fp32 [batch][num_kv_heads][mass_tokens], 16-byte aligned,
  * mass_tokens a multiple of 4 and at least 16 * max_blocks_per_seq. mass_in may be mass_out (only
  * visible positions are then touched) or NULL (zero); it may not overlap it otherwise. ws: at least the
  * matching workspace size (it holds a score per query head and position: 4 * batch * num_q_heads * 16 *
