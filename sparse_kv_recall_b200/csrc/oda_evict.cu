@@ -11,15 +11,16 @@
 // counts, so the result does not depend on any order of execution. Up to kAlone slots every CTA of the
 // cluster selects by itself, from all the keys, and moves its share of the rows: a pass is then two CTA
 // barriers, where histograms summed through distributed shared memory cost a cluster barrier and a remote
-// read (2304 slots, budget 2048, one sequence of 8 KV heads: 22.9 us with shared histograms, 13.3 so).
+// read (2304 slots, budget 2048, one sequence of 8 KV heads: 23.1 us with shared histograms, 13.0 so).
 // Longer sequences are shared out over the cluster.
 //
 // Bound: memory for the rows -- a kept row is read and written once (512 bytes in bf16, 144 in 4 bits), a
 // weight is read a few times, mostly out of L2 or shared memory -- and before them, not overlapped, the
 // selection's chain of barriers and scans. Four sequences of 20K to 32K cut down to 4096 (135 MB of bf16 rows):
 // 44.5 us, of which the move takes 19, at the rate of a copy, and the selection 20; 16 sequences of 1.5K to
-// 8K in 4 bits down to 2049: 35.7 us, 13 of them the move. (Fetching the recent rows, which move in any case,
-// into L2 beside the selection: 48.5 us for the former.)
+// 8K in 4 bits down to 2049: 34.7 us, 13 of them the move. (Fetching the recent rows, which move in any case,
+// into L2 beside the selection: 48.5 us for the former.) In place, with a barrier before each round's stores:
+// 49.5, 36.5, and 13.7 for the 2304 slots.
 //
 // In place, a move must not overwrite a row that has not been read. The i-th kept slot p_i is >= i,
 // so when the rows of a round, a run [i0, i1) of the kept list, are all in registers before the
@@ -107,8 +108,17 @@ __device__ __forceinline__ unsigned warp_scan(unsigned v, int lane) {  // inclus
 }
 
 constexpr int kKeyCache = 8192;  // keys held in shared memory (a CTA's share of more is read again)
-constexpr int kAlone = 4096;     // slots up to which each CTA of a cluster selects by itself (2304: 13.3 us,
-                                 // shared 23.1; 8K in 4 bits, two CTAs a cluster: 37.4 us, shared 35.7)
+// Slots up to which each CTA of a cluster selects by itself. Sequences of n slots cut down to n / 2, 8 KV heads, us
+// alone / shared:
+//   n                             1100         2304         3600         4090         5000         6000         8000
+//   bf16, 1 sequence, 16 CTAs   9.8 / 14.0  13.2 / 23.1  16.3 / 23.5  16.9 / 23.6  22.7 / 27.6  25.4 / 28.3  29.5 / 29.0
+//   bf16, 4 sequences, 8       12.3 / 18.8  24.5 / 23.7  24.6 / 25.8  24.4 / 27.1  34.9 / 30.9  33.8 / 32.8  42.9 / 38.9
+//   bf16, 16 sequences, 2      21.6 / 25.1  37.7 / 40.1  56.0 / 56.4  61.0 / 61.1  74.0 / 72.8  87.0 / 85.3   113 / 109
+//   4 bits, 1 sequence, 16     10.5 / 14.8  14.5 / 23.6  17.5 / 23.9  18.1 / 23.8  20.1 / 24.2  22.0 / 24.3  25.6 / 24.6
+//   4 bits, 4 sequences, 8     15.8 / 19.1  16.4 / 19.4  20.6 / 20.7  19.6 / 21.0  21.9 / 22.4  24.1 / 23.2  43.2 / 28.0
+//   4 bits, 16 sequences, 2    14.5 / 17.5  21.2 / 23.3  27.6 / 28.2  31.4 / 31.8  36.6 / 36.0  43.5 / 42.3  55.6 / 53.6
+// (Where 16 CTAs share one sequence's head, alone is faster up to about 7000.)
+constexpr int kAlone = 4096;
 
 constexpr int kFew = 128;     // keys that are compared with one another directly, by four threads each
 constexpr int kAhead = 6;     // weights a thread has in flight (2304 slots: 13.3 us with 4 or 6, 13.9 with 8;
