@@ -586,7 +586,6 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
   const int each = Pe > 0 ? T / Pe : 0, more = Pe > 0 ? T % Pe : 0;
   const int share_end = cta < Pe ? (cta + 1) * each + (cta + 1) * more / Pe : 0;
   int x = cta < Pe ? cta * each + cta * more / Pe : 0;
-  const uint64_t policy = l2_evict_first_policy();
 
   // (Whatever a piece or a CTA does once is written at one place in these loops: at several, inlined, it made
   // the kernel 108 KB of code, much of whose first execution waited for the instruction cache.)
@@ -623,8 +622,9 @@ __global__ void __launch_bounds__(kThreads4, kCtasPerSm4)
     auto issue = [&](int s) {  // one group of copies a step, empty past the last
       if (s < steps) {
         const ulonglong2 src = *reinterpret_cast<const ulonglong2*>(&refs.src[2 * s % kRefs4]);
+        // (the policy made anew each time: held in two registers it costs 1 to 3 % of a long call)
         kv4_copy(smem_addr(stages) + (s & 1) * kStageBytes4, reinterpret_cast<const unsigned char*>(src.x),
-                 reinterpret_cast<const unsigned char*>(src.y), lane, policy);
+                 reinterpret_cast<const unsigned char*>(src.y), lane, l2_evict_first_policy());
       }
       copies_commit();
     };
