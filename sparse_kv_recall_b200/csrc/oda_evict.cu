@@ -18,9 +18,9 @@
 // weight is read a few times, mostly out of L2 or shared memory -- and before them, not overlapped, the
 // selection's chain of barriers and scans. Four sequences of 20K to 32K cut down to 4096 (135 MB of bf16 rows):
 // 44.5 us, of which the move takes 19, at the rate of a copy, and the selection 20; 16 sequences of 1.5K to
-// 8K in 4 bits down to 2049: 34.7 us, 13 of them the move. (Fetching the recent rows, which move in any case,
+// 8K in 4 bits down to 2049: 34.9 us, 13 of them the move. (Fetching the recent rows, which move in any case,
 // into L2 beside the selection: 48.5 us for the former.) In place, with a barrier before each round's stores:
-// 49.5, 36.5, and 13.7 for the 2304 slots.
+// 50.3, 36.7, and 13.7 for the 2304 slots.
 //
 // In place, a move must not overwrite a row that has not been read. The i-th kept slot p_i is >= i,
 // so when the rows of a round, a run [i0, i1) of the kept list, are all in registers before the

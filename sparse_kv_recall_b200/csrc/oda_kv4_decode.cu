@@ -26,10 +26,10 @@
 // fp16 add or fma that takes the offset off.
 //
 // Measured (one B200, calls replayed from a graph, bf16 or fp32 out; 8 KV heads): one sequence of 131,073 tokens, 16
-// query heads, 151 MB, 36.7 us (4.1 TB/s; some 10 of them before the first and after the last page); eight of
-// 16,385, 39.9 us; sixteen of 8K to 64K, 32 query heads, 721 MB, 153.5 us (4.7 TB/s, 73 % of a copy's rate), and
-// 170 us (4.2 TB/s, 65 %) where calls follow one another for long enough that the power cap lowers the clock. Two
-// query heads per KV head: 59 % of the issue slots and 45 % of DRAM; four: 65 % and 54 %. Eight warps of two CTAs an SM and two
+// query heads, 151 MB, 36.0 us (4.2 TB/s; some 10 of them before the first and after the last page); eight of
+// 16,385, 39.3 us; sixteen of 8K to 64K, 32 query heads, 721 MB, 148.2 us (4.9 TB/s, 75 % of a copy's rate), and
+// 163 us (4.4 TB/s, 68 %) where calls follow one another for long enough that the power cap lowers the clock. Two
+// query heads per KV head: 58 % of the issue slots and 47 % of DRAM; four: 66 % and 59 %. Eight warps of two CTAs an SM and two
 // pages a step are what 128 registers a thread and the stages leave; nine to twelve warps spill.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -487,15 +487,15 @@ __device__ __forceinline__ int kv4_refs(const Kv4Params& p, const Piece& piece, 
   return seen;
 }
 
-// Called, not inlined: what a step needs rarely keeps its registers and code to itself (no faster: 128K history 36.7 us
-// either way, ragged 8K..64K batch 153.8, 153.6 inlined).
+// Called, not inlined: what a step needs rarely keeps its registers and code to itself (128K history 36.0 us
+// either way, ragged 8K..64K batch 148.4, 148.8 inlined).
 __device__ __noinline__ int kv4_refs_call(const Kv4Params& p, const Piece& piece, PageRefs& refs, int n0, int warp,
                                           int lane) {
   return kv4_refs(p, piece, refs, n0, warp, lane);
 }
 
 // One warp, a step that holds the page of slot t: the step's K/V, quantised, take the slot in the cache and
-// in this copy. (Inlined: the Local call of one 4K sequence, sink 4 and window 256, 8.1 us, called 8.4.)
+// in this copy. (Inlined or called, the Local call of one 4K sequence, sink 4 and window 256, takes 7.9 to 8.4 us.)
 __device__ __forceinline__ void kv4_commit(const Kv4Params& p, const Piece& piece, const PageRefs& refs, int s,
                                         unsigned char* stage, int lane) {
 #pragma unroll 1

@@ -7,9 +7,9 @@
 // 256 bytes in bf16, 72 in 4 bits) and a second kernel, launched with a programmatic dependency,
 // turns scores into weights and adds them up over the query heads of the KV head. Bound: latency (length,
 // page and scores, then the weights' store) and memory, 4 G + 8 bytes per position and KV head, the scores
-// mostly out of L2. Two sequences of 32,769 tokens, 8 KV heads, 32 query heads: 60.4 us in all, 53.4 of them the
-// bf16 attention by itself (60.2 with mass_in as mass_out); eight of 9K to 16K in 4 bits, 16 query heads: 37.9,
-// of them 32.1 (37.8).
+// mostly out of L2. Two sequences of 32,769 tokens, 8 KV heads, 32 query heads: 60.6 us in all, 53.6 of them the
+// bf16 attention by itself (60.3 with mass_in as mass_out); eight of 9K to 16K in 4 bits, 16 query heads: 38.0,
+// of them 31.7 (37.8).
 #include <math.h>
 
 #include "oda_decode.cuh"
