@@ -33,9 +33,15 @@ __global__ void __launch_bounds__(kMergeThreads) merge_partials_kernel(const Mer
   __shared__ float s_m, s_sum;
   if (tid < 32) {
     float m = -INFINITY;
-    for (int r = tid; r < p.parts; r += 32) m = fmaxf(m, p.lse_parts[r * rows + row]);
+    bool any = false;  // some part is not empty: its log-sum is a number, or a NaN, which a maximum passes over
+    for (int r = tid; r < p.parts; r += 32) {
+      const float l = p.lse_parts[r * rows + row];
+      m = fmaxf(m, l);
+      any |= l != -INFINITY;
+    }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (__any_sync(0xffffffffu, any) && m == -INFINITY) m = 0.f;  // (NaNs alone: the result is NaN)
     float sum = 0.f;
     for (int r = tid; r < p.parts; r += 32) {
       const float l = p.lse_parts[r * rows + row];

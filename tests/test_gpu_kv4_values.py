@@ -188,3 +188,17 @@ def test_a_nan_in_q_shows_in_the_weights(kv4, G):
     for b, n in enumerate(lens):
         assert torch.isnan(mass[b, 1, :n]).all() and (mass[b, :, n:] == 2.0).all()
         assert np.abs(mass[b, 0, :n].double().cpu().numpy() - 2.0 - want[b][1][0]).max() <= MASS + 2.0 ** -22
+
+
+def test_a_nan_shows_when_shards_are_merged():
+    """Parts of a history by 4-bit shards, some past its end (empty): a head whose scores are NaN stays NaN."""
+    c = PagedCase([700, 3000], 4, 2, seed=460)
+    ref, rlse, _ = c.oracle(lambda b, t: O.full_positions(t))
+    c.q[:, 3, 5] = float("nan")
+    parts = [_decode(c, oda.shard_visibility(lo, hi)) for lo, hi in ((0, 256), (256, 1024), (1024, 4096), (4096, 8192))]
+    out, lse = c.out(fill=3.0)
+    oda.oda_merge_partials(torch.stack([o for o, _ in parts]), torch.stack([l for _, l in parts]), out, lse=lse)
+    c.ok()
+    assert torch.isnan(out[:, 3]).all() and torch.isnan(lse[:, 3]).all()
+    assert_out_close(out[:, :3], ref[:, :3])
+    assert_lse_close(lse[:, :3].cpu().numpy(), rlse[:, :3])
