@@ -29,8 +29,8 @@
 // query heads, 151 MB, 36.0 us (4.2 TB/s; some 10 of them before the first and after the last page); eight of
 // 16,385, 39.3 us; sixteen of 8K to 64K, 32 query heads, 721 MB, 148.2 us (4.9 TB/s, 75 % of a copy's rate), and
 // 163 us (4.4 TB/s, 68 %) where calls follow one another for long enough that the power cap lowers the clock. Two
-// query heads per KV head: 58 % of the issue slots and 47 % of DRAM; four: 66 % and 59 %. Eight warps of two CTAs an SM and two
-// pages a step are what 128 registers a thread and the stages leave; nine to twelve warps spill.
+// query heads per KV head: 58 % of the issue slots and 47 % of DRAM; four: 66 % and 59 %. Eight warps of two CTAs
+// an SM and two pages a step are what 128 registers a thread and the stages leave; nine to twelve warps spill.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -158,7 +158,7 @@ constexpr float kRoom = 7.f;  // scores stay this far below m: a weight times a 
                               // hundred of them, is inside fp32 for the largest bf16 values too
 
 // The group's q as B fragments (scaled to q') and, for the lane's own head, 2^-14 sum q' of each group and the
-// factor that undoes q's power of two and the codes' 2^-14. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
+// factor that undoes q's power of two. K step s takes nibbles 2 (s & 1), 2 (s & 1) + 1 and those four further up of
 // word e = s / 2 of the lane's 16-byte code chunk, which is all group e & 1.
 template <int G>
 __device__ __forceinline__ void load_q4(const __nv_bfloat16* q, int lane, uint4 (&v)[4]) {
