@@ -28,7 +28,7 @@
 // Measured (one B200, calls replayed from a graph, bf16 or fp32 out; 8 KV heads): one sequence of 131,073 tokens, 16
 // query heads, 151 MB, 36.0 us (4.2 TB/s; some 10 of them before the first and after the last page); eight of
 // 16,385, 39.3 us; sixteen of 8K to 64K, 32 query heads, 721 MB, 148.2 us (4.9 TB/s, 75 % of a copy's rate), and
-// 163 us (4.4 TB/s, 68 %) where calls follow one another for long enough that the power cap lowers the clock. Two
+// 163 to 170 us (4.3 TB/s, 67 %) where calls follow one another for long enough that the power cap lowers the clock. Two
 // query heads per KV head: 58 % of the issue slots and 47 % of DRAM; four: 66 % and 59 %. Eight warps of two CTAs
 // an SM and two pages a step are what 128 registers a thread and the stages leave; nine to twelve warps spill.
 #include <cuda_fp16.h>
